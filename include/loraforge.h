@@ -436,6 +436,153 @@ lf_status lf_lora_shrink_expand_noalloc(int32_t T, int32_t d_in, int32_t d_out,
                                         int64_t pool_elems_A, int64_t pool_elems_Bt,
                                         float scale, int32_t* seg_out, lf_stream_t stream);
 
+/* ---- Routing tokens to experts ------------------------------------------------
+ * A gate that picks adapters per token instead of a fixed adapter id (the dynamic side
+ * of "static and dynamic multi-LoRA composition", LoRASpace, the arXiv listing's
+ * abstract).  For every token t with logits l_e (T rows of logits_ld elements of
+ * logits_type, E = n_experts of them used):
+ *   s_e  = softmax(l)_e (score 0) or 1 / (1 + exp(-l_e)) (score 1)
+ *   c_e  = s_e + bias_e: what the choice goes by; the weights never see the bias.
+ *          Without a bias c_e orders the experts as l_e does, and l_e decides.
+ *   n_groups > 1: the experts are cut into n_groups equal runs; a group's score is its
+ *          largest c (group_top 1) or the sum of its two largest (group_top 2; the only
+ *          one there is counts alone); the top_groups best groups stay.
+ *   ids[t][0 .. top_k): the experts with the largest c, in descending order;
+ *   weights[t][j] = weight_scale * s (renorm 0) or weight_scale * s / sum of the chosen s
+ *          (renorm 1; formed from ratios, so chosen scores that underflow keep theirs).
+ * Ties, of experts and of groups, go to the lower index, and the choice is the one of
+ * exact arithmetic: rows whose order fp32 cannot settle are decided in fp64.
+ * Only a logit or bias of -inf shuts an expert out (a finite lowest value does not); where
+ * fewer than top_k experts remain the last slots are id -1, weight 0, the form
+ * lf_lora_mixture skips.  A NaN or +inf in a row's logits or in the bias latches
+ * LF_ERR_NUMERIC and leaves the row all -1.  Scores and weights are formed in fp32.
+ * counts (nullable, E int32) receives how many slots chose each expert (for balancing).
+ * lf_route_experts_backward: grad_logits (T rows of grad_ld, logits_type) from
+ * grad_weights (T x top_k fp32) at the same logits and the forward's ids; the choice and
+ * the bias have no gradient, slots of -1 are skipped, an id out of range latches
+ * LF_ERR_BAD_INDEX and is skipped.  Every entry 0 .. E of every row is written.
+ * Errors: LF_ERR_INVALID_ARG (null pointers, negative T, unknown score / type / flag,
+ * a weight_scale that is not finite, row strides below E), LF_ERR_SHAPE (E outside
+ * 1 .. LF_ROUTER_MAX_EXPERTS, top_k outside 1 .. min(E, LF_ROUTER_MAX_K), n_groups not a
+ * divisor of E or above 32, top_groups outside 1 .. n_groups, group_top outside 1 .. 2).
+ * Pointers need the alignment of their element type only. */
+#define LF_ROUTER_MAX_EXPERTS 1024
+#define LF_ROUTER_MAX_K 16
+enum { LF_F32 = 0, LF_BF16 = 1, LF_F16 = 2 };   /* element types */
+typedef struct {
+    int32_t n_experts, top_k;
+    int32_t score;                 /* 0 softmax, 1 sigmoid */
+    int32_t n_groups, top_groups;  /* 1, 1 = no groups */
+    int32_t group_top;             /* 1 or 2 */
+    int32_t renorm;                /* 0 or 1 */
+    float weight_scale;
+} lf_router;
+lf_status lf_route_experts(int32_t T, const lf_router* router /*[host]*/, const void* logits, int32_t logits_type,
+                           int64_t logits_ld, const float* bias, int32_t* ids, float* weights, int32_t* counts,
+                           lf_stream_t stream);
+lf_status lf_route_experts_backward(int32_t T, const lf_router* router /*[host]*/, const void* logits,
+                                    int32_t logits_type, int64_t logits_ld, const int32_t* ids,
+                                    const float* grad_weights, void* grad_logits, int64_t grad_ld,
+                                    lf_stream_t stream);
+
+/* ---- Routed (mixture) side path -----------------------------------------------
+ * The experts' products: every token carries top_k slots (adapter id, weight), and for
+ * every token t and projection p
+ *   y_t[..] = bf16( base_t[..] + sum_j w_tj s_j B'_{e_tj} (A'_{e_tj} x_t) )
+ * over the slots with e_tj = ids[t][j] >= 0, with s_j = adapter_scale[e_tj] when
+ * adapter_scale (n_adapters floats) is not NULL, else `scale`; fp32 intermediates, one
+ * rounding.  weights (T x top_k fp32) may be NULL (all 1).  A slot of -1 contributes
+ * nothing (its weight is not read); the same adapter in two slots counts twice; an id
+ * outside -1 .. n_adapters - 1 latches LF_ERR_BAD_INDEX and its slot contributes nothing,
+ * as does a slot whose factors fail the checks of lf_lora_shrink_expand.
+ * base: T rows of y_ld, read at the slice's columns; NULL = zeros; may be y itself (in
+ * place), else must not overlap y.  Columns of y outside the slice are not written; every
+ * row of the slice is (a token without valid slots gets its base row).
+ * x: T rows of x_ld elements (multiple of 8).  Factor tables, pools, y_offset and max_rank
+ * as for lf_lora_shrink_expand_slices.  1 <= top_k <= LF_ROUTER_MAX_K.  Projections of one
+ * call must not write overlapping parts of any y, nor a y that another one reads.
+ * lf_lora_mixture_backward: gradients with the adapters held fixed (they are compressed
+ * after training), per projection from dy (T rows of dy_ld, read at the slice's columns):
+ *   dx_t = bf16( dx_base_t + sum_j w_tj s_j A'^T (B'^T dy_t) )   (dx NULL = not wanted;
+ *          dx_base NULL = zeros, may be dx itself)
+ *   grad_weights[t][j] = sum over the call's projections of s_j <B'^T dy_t, A'_{e_tj} x_t>
+ *          (fp32, projections in order; slots of -1 get 0; NULL = not wanted).
+ * Workspace for either: lf_lora_mixture_workspace_size(T, top_k, n_adapters, n_proj,
+ * max_rank), max_rank = the largest max_rank of the projections (0 where one is 0);
+ * 0 bytes when none is needed (ws may then be NULL).  Results are the same from run to
+ * run; a batch size may change the order of sums. */
+typedef struct {
+    const void* x;              /* T rows of x_ld bf16 */
+    const void* base;           /* nullable: T rows of y_ld bf16 */
+    void* y;                    /* T rows of y_ld bf16 */
+    int32_t d_in;
+    int32_t reserved;           /* 0 */
+    int64_t x_ld, y_ld;
+    lf_slice slice;
+} lf_mixture_projection;
+typedef struct {
+    const void* x;              /* T rows of x_ld bf16 */
+    const void* dy;             /* T rows of dy_ld bf16 */
+    const void* dx_base;        /* nullable: T rows of dx_ld bf16 */
+    void* dx;                   /* nullable: T rows of dx_ld bf16 */
+    int32_t d_in;
+    int32_t reserved;           /* 0 */
+    int64_t x_ld, dy_ld, dx_ld;
+    lf_slice slice;             /* y_offset: first column of the slice in dy */
+} lf_mixture_grad;
+size_t lf_lora_mixture_workspace_size(int32_t T, int32_t top_k, int32_t n_adapters, int32_t n_proj, int32_t max_rank);
+lf_status lf_lora_mixture(int32_t T, int32_t top_k, const int32_t* ids, const float* weights, int32_t n_adapters,
+                          const lf_mixture_projection* projs /*[host]*/, int32_t n_proj, float scale,
+                          const float* adapter_scale, void* ws, size_t ws_bytes, lf_stream_t stream);
+lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids, const float* weights,
+                                   int32_t n_adapters, const lf_mixture_grad* projs /*[host]*/, int32_t n_proj,
+                                   float scale, const float* adapter_scale, float* grad_weights, void* ws,
+                                   size_t ws_bytes, lf_stream_t stream);
+
+/* ---- Base weights in 4 bits ----------------------------------------------------
+ * The W0 x under the side path ("Compress then Serve", section 3: (W0 + B A) x), with W0
+ * held as 4-bit codes with one scale (and optionally one zero point) per group of `group`
+ * consecutive columns of a row; group is 32, 64, 128 or 256, d_in a multiple of 32, and
+ * the last group of a row may be short (ng = ceil(d_in / group)):
+ *   q      d_out x d_in / 2 bytes, column 2c in the low nibble of byte c;
+ *   scales d_out x ng bf16;   zeros  d_out x ng bytes, 0 .. 15 (higher bits are ignored),
+ *   or NULL = 8 everywhere;   W0[r][c] = (q[r][c] - zeros[r][g]) * scales[r][g].
+ * lf_w4_quantize: from W (d_out x d_in, fp32 / bf16 / fp16).  zeros NULL: scale =
+ * bf16(max|w| / 7), else scale = bf16((max(w, 0) - min(w, 0)) / 15) and zero =
+ * clamp(rint(-min(w, 0) / scale), 0, 15); code = clamp(rint(w / scale) + zero, 0, 15);
+ * quotients are exact before they are rounded, halves go to even; a group of zeros (or one
+ * whose scale rounds to 0) has scale 0 and, with zeros, zero 0.  A value that is not
+ * finite counts as 0 and latches LF_ERR_NUMERIC.
+ * lf_w4_dequantize: W0 to fp32 (exact), bf16 or fp16 (rounded once).
+ * lf_w4_projections: for up to LF_MAX_PROJECTIONS projections of one token batch, in one
+ * call, y_t = bf16( bias + sum_g scale_g sum_{c in g} (q_c - zero_g) x_tc ): products
+ * exact, sums in fp32, one rounding.  bias: nullable, d_out bf16.  x: T rows of x_ld, y: T
+ * rows of y_ld, of which columns 0 .. d_out are written; x_ld and y_ld are multiples of 8;
+ * projections may share x, but no y may overlap another y or an x.
+ * Workspace: lf_w4_workspace_size(T, projs, n_proj) bytes (0: ws may be NULL).
+ * Errors: LF_ERR_INVALID_ARG (null pointers, negative counts, unknown type, x_ld < d_in,
+ * y_ld < d_out, reserved not 0), LF_ERR_SHAPE (d_in not a positive multiple of 32, d_out < 1, another group),
+ * LF_ERR_ALIGNMENT (q, x, y, W not 16-byte aligned, scales or bias not 2-byte aligned,
+ * d_out, x_ld or y_ld not a multiple of 8), LF_ERR_WORKSPACE. */
+typedef struct {
+    const void* x;              /* T rows of x_ld bf16 */
+    void* y;                    /* T rows of y_ld bf16 */
+    const void* q;              /* d_out x d_in / 2 bytes */
+    const void* scales;         /* d_out x ng bf16 */
+    const void* zeros;          /* nullable: d_out x ng bytes */
+    const void* bias;           /* nullable: d_out bf16 */
+    int32_t d_in, d_out, group;
+    int32_t reserved;           /* 0 */
+    int64_t x_ld, y_ld;
+} lf_w4_projection;
+lf_status lf_w4_quantize(const void* W, int32_t W_type, int32_t d_out, int32_t d_in, int32_t group, void* q,
+                         void* scales, void* zeros, lf_stream_t stream);
+lf_status lf_w4_dequantize(const void* q, const void* scales, const void* zeros, int32_t d_out, int32_t d_in,
+                           int32_t group, void* W, int32_t W_type, lf_stream_t stream);
+size_t lf_w4_workspace_size(int32_t T, const lf_w4_projection* projs /*[host]*/, int32_t n_proj);
+lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs /*[host]*/, int32_t n_proj, void* ws,
+                            size_t ws_bytes, lf_stream_t stream);
+
 /* ---- Tracing (no counterpart on the pages: measurement support) --------------
  * Every kernel launch of the library is counted.  With timing enabled, each
  * launch is also bracketed by CUDA events recorded on its own stream and its

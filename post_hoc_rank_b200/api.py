@@ -2,6 +2,7 @@
 tensors and calls the binding.  No arithmetic of the method happens here."""
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 
 import numpy as np
@@ -213,6 +214,160 @@ def jd_full(mods, tabs: JdTables, B_base, A_base, U, Vt, iters: int, weights=Non
     ws = ws if ws is not None else workspace(lf.lf_jd_workspace_size(mods, tabs.members, tabs.probs), U.device)
     lf.lf_jd_full(mods, tabs.members, tabs.probs, B_base, A_base, weights, iters, U, Vt, sigma, ws, stream)
     return U, Vt, sigma
+
+
+# ---- routed side path and 4-bit base weights ------------------------------------------------
+
+def _on(device):
+    """Context in which `device` is the current one (kernels launch on its current stream)."""
+    if device.type != "cuda":
+        raise ValueError(f"tensors must live on a CUDA device, got {device}")
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def _expect(t, name: str, device, dtype, shape):
+    if t is not None and (t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or
+                          not t.is_contiguous()):
+        raise ValueError(f"{name}: contiguous {dtype} tensor of shape {tuple(shape)} on {device} expected")
+
+
+def _check_logits(logits, router: lf.lf_router):
+    if logits.dim() != 2 or logits.shape[1] != router.n_experts or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits must be T x {router.n_experts} with unit column stride, got {tuple(logits.shape)}")
+    if logits.shape[0] > 1 and logits.stride(0) < logits.shape[1]:
+        raise ValueError("logits rows must not overlap")
+
+
+def route_experts(logits, router: lf.lf_router, bias=None, counts=None, stream=None):
+    """Experts and weights of every token (lf_route_experts; lf.make_router): ids T x top_k int32
+    (-1 = empty slot) and weights T x top_k fp32.  bias: fp32 per expert, steers the choice only;
+    counts: int32 per expert, overwritten with the number of slots that chose it."""
+    _check_logits(logits, router)
+    T, dev = logits.shape[0], logits.device
+    _expect(bias, "bias", dev, torch.float32, (router.n_experts,))
+    _expect(counts, "counts", dev, torch.int32, (router.n_experts,))
+    with _on(dev):
+        ids = torch.empty((T, router.top_k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, router.top_k), dtype=torch.float32, device=dev)
+        lf.lf_route_experts(logits, router, bias, ids, weights, counts, stream)
+    return ids, weights
+
+
+def route_experts_backward(logits, router: lf.lf_router, ids, grad_weights, stream=None):
+    """Gradient of route_experts' weights for the logits (same type), at its ids."""
+    _check_logits(logits, router)
+    T, dev = logits.shape[0], logits.device
+    _expect(ids, "ids", dev, torch.int32, (T, router.top_k))
+    _expect(grad_weights, "grad_weights", dev, torch.float32, (T, router.top_k))
+    with _on(dev):
+        grad = torch.empty((T, router.n_experts), dtype=logits.dtype, device=dev)
+        lf.lf_route_experts_backward(logits, router, ids, grad_weights, grad, stream)
+    return grad
+
+
+def _same_rows(projections, T: int):
+    if any(p.rows != T for p in projections):
+        raise ValueError(f"every projection must have {T} rows, got {[p.rows for p in projections]}")
+
+
+def _mixture_ws(ids, n_adapters: int, projections):
+    ranks = [p.slice.max_rank for p in projections]
+    n = lf.lf_lora_mixture_workspace_size(ids.shape[0], ids.shape[1], n_adapters, len(projections),
+                                          0 if 0 in ranks else max(ranks))
+    return workspace(n, ids.device) if n else None
+
+
+def lora_mixture(ids, weights, n_adapters: int, projections, scale: float, adapter_scale=None, ws=None, stream=None):
+    """Routed side path (lf_lora_mixture) of lf.make_mixture_projection projections, whose y it
+    writes: y = base + scale * sum_j weights_j B'_j (A'_j x).  ids T x top_k int32 (-1 = empty
+    slot), weights T x top_k fp32 or None (all 1), as route_experts returns them."""
+    dev = ids.device
+    _expect(ids, "ids", dev, torch.int32, ids.shape)
+    _expect(weights, "weights", dev, torch.float32, ids.shape)
+    _expect(adapter_scale, "adapter_scale", dev, torch.float32, (n_adapters,))
+    _same_rows(projections, ids.shape[0])
+    with _on(dev):
+        ws = ws if ws is not None else _mixture_ws(ids, n_adapters, projections)
+        lf.lf_lora_mixture(ids, weights, n_adapters, projections, scale, ws, adapter_scale, stream)
+
+
+def lora_mixture_backward(ids, weights, n_adapters: int, grads, scale: float, adapter_scale=None, grad_weights=True,
+                          ws=None, stream=None):
+    """Gradients of lora_mixture (lf_lora_mixture_backward): writes the dx of every
+    lf.make_mixture_grad entry and returns the weights' gradient (T x top_k fp32, summed over the
+    entries), or None with grad_weights=False."""
+    dev = ids.device
+    _expect(ids, "ids", dev, torch.int32, ids.shape)
+    _expect(weights, "weights", dev, torch.float32, ids.shape)
+    _expect(adapter_scale, "adapter_scale", dev, torch.float32, (n_adapters,))
+    _same_rows(grads, ids.shape[0])
+    with _on(dev):
+        gw = torch.empty(ids.shape, dtype=torch.float32, device=dev) if grad_weights else None
+        ws = ws if ws is not None else _mixture_ws(ids, n_adapters, grads)
+        lf.lf_lora_mixture_backward(ids, weights, n_adapters, grads, scale, gw, ws, adapter_scale, stream)
+    return gw
+
+
+@dataclasses.dataclass
+class W4:
+    """A base weight matrix in 4 bits: (q - zeros) * scales per group of columns."""
+    q: torch.Tensor               # uint8 [d_out, d_in / 2], even columns in the low nibbles
+    scales: torch.Tensor          # bf16 [d_out, ng]
+    zeros: torch.Tensor | None    # uint8 [d_out, ng], None = 8
+    group: int
+
+    @property
+    def shape(self):
+        return self.q.shape[0], 2 * self.q.shape[1]
+
+
+def w4_quantize(W, group: int = 128, zero_points: bool = False, stream=None) -> W4:
+    """Quantises W (d_out x d_in fp32, bf16 or fp16) to 4 bits with a scale, and with
+    zero_points a zero point, per `group` columns (lf_w4_quantize)."""
+    if W.dim() != 2 or not W.is_contiguous():
+        raise ValueError("W must be a contiguous matrix")
+    if group not in (32, 64, 128, 256):
+        raise ValueError(f"group must be 32, 64, 128 or 256, got {group}")
+    d_out, d_in = W.shape
+    dev, ng = W.device, (d_in + group - 1) // group
+    with _on(dev):
+        out = W4(torch.empty((d_out, d_in // 2), dtype=torch.uint8, device=dev),
+                 torch.empty((d_out, ng), dtype=torch.bfloat16, device=dev),
+                 torch.empty((d_out, ng), dtype=torch.uint8, device=dev) if zero_points else None, group)
+        lf.lf_w4_quantize(W, group, out.q, out.scales, out.zeros, stream)
+    return out
+
+
+def w4_dequantize(w4: W4, dtype=torch.bfloat16, stream=None):
+    """The matrix a W4 stands for (lf_w4_dequantize), fp32 (exact), bf16 or fp16."""
+    dev = w4.q.device
+    with _on(dev):
+        W = torch.empty(w4.shape, dtype=dtype, device=dev)
+        lf.lf_w4_dequantize(w4.q, w4.scales, w4.zeros, w4.group, W, stream)
+    return W
+
+
+def w4_project(projections, ws=None, stream=None):
+    """y = x W0^T + bias for lf.make_w4_projection projections of one token batch
+    (lf_w4_projections): all have the same number of rows of x."""
+    T = projections[0].rows
+    _same_rows(projections, T)
+    dev = projections[0].device
+    with _on(dev):
+        if ws is None:
+            n = lf.lf_w4_workspace_size(T, projections)
+            ws = workspace(n, dev) if n else None
+        lf.lf_w4_projections(T, projections, ws, stream)
+
+
+def w4_linear(x, w4: W4, bias=None, out=None, stream=None):
+    """x (T x d_in bf16) times a 4-bit matrix: T x d_out bf16 (lf_w4_projections, one projection)."""
+    if x.shape[1] != w4.shape[1]:
+        raise ValueError(f"x has {x.shape[1]} columns, the matrix {w4.shape[1]}")
+    with _on(x.device):
+        y = out if out is not None else torch.empty((x.shape[0], w4.shape[0]), dtype=torch.bfloat16, device=x.device)
+        w4_project([lf.make_w4_projection(x, y, w4.q, w4.scales, w4.group, w4.zeros, bias)], stream=stream)
+    return y
 
 
 def device_status(stream=None) -> int:

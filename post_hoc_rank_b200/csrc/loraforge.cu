@@ -3,6 +3,7 @@
 // word needs no relocatable device code.
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <cstring>
 #include <map>
 #include <mutex>
@@ -17,6 +18,9 @@
 #include "apply.cuh"
 #include "jd.cuh"
 #include "pool.cuh"
+#include "router.cuh"
+#include "mixture.cuh"
+#include "w4.cuh"
 
 namespace lf {
 
@@ -980,7 +984,163 @@ static lf_status check_pool(int32_t side, int32_t n_lora, const int32_t* ranks, 
     *R_out = (int32_t)R;
     return LF_OK;
 }
+
+// ------------------------------------------------------------------ routing to experts
+static lf_status check_router(int32_t T, const lf_router* r, const void* logits, int32_t type, int64_t ld) {
+    if (T < 0 || !r) return LF_ERR_INVALID_ARG;
+    if (r->score < 0 || r->score > 1 || r->renorm < 0 || r->renorm > 1 || type < LF_F32 || type > LF_F16 ||
+        !std::isfinite(r->weight_scale))
+        return LF_ERR_INVALID_ARG;
+    if (r->n_experts < 1 || r->n_experts > LF_ROUTER_MAX_EXPERTS || r->top_k < 1 || r->top_k > r->n_experts ||
+        r->top_k > LF_ROUTER_MAX_K || r->n_groups < 1 || r->n_groups > 32 || r->n_experts % r->n_groups != 0 ||
+        r->top_groups < 1 || r->top_groups > r->n_groups || r->group_top < 1 || r->group_top > 2)
+        return LF_ERR_SHAPE;
+    if (T > 0 && (!logits || ld < r->n_experts)) return LF_ERR_INVALID_ARG;
+    const uintptr_t es = type == LF_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(logits) % es) return LF_ERR_ALIGNMENT;
+    return LF_OK;
+}
+
+static bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+template <typename TL, int EPL>
+static cudaError_t launch_router(const RouterArgs& a, cudaStream_t s) {
+    const bool scores = a.bias != nullptr || (a.G > 1 && a.group_top == 2);
+    const size_t sm = scores ? (size_t)kRouterWarps * a.E * sizeof(double) : 0;
+    if (sm > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(route_experts_kernel<TL, EPL>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+        if (e != cudaSuccess) return e;
+    }
+    LF_LAUNCH("route_experts", (route_experts_kernel<TL, EPL>), (unsigned)cdiv(a.T, kRouterWarps), 32 * kRouterWarps, sm,
+              s, a);
+    return cudaGetLastError();
+}
+template <typename TL, int EPL>
+static cudaError_t launch_router(const RouterGradArgs& a, cudaStream_t s) {
+    LF_LAUNCH("route_experts_grad", (route_experts_grad_kernel<TL, EPL>), (unsigned)cdiv(a.T, kRouterWarps),
+              32 * kRouterWarps, 0, s, a);
+    return cudaGetLastError();
+}
+// registers per lane: the power of two that holds the row
+template <typename TL, typename ARGS>
+static cudaError_t launch_router_epl(const ARGS& a, cudaStream_t s) {
+    if (a.E <= 32) return launch_router<TL, 1>(a, s);
+    if (a.E <= 64) return launch_router<TL, 2>(a, s);
+    if (a.E <= 128) return launch_router<TL, 4>(a, s);
+    if (a.E <= 256) return launch_router<TL, 8>(a, s);
+    if (a.E <= 512) return launch_router<TL, 16>(a, s);
+    return launch_router<TL, 32>(a, s);
+}
+template <typename ARGS>
+static cudaError_t launch_router_type(int32_t type, const ARGS& a, cudaStream_t s) {
+    if (type == LF_F32) return launch_router_epl<float>(a, s);
+    if (type == LF_BF16) return launch_router_epl<__nv_bfloat16>(a, s);
+    return launch_router_epl<__half>(a, s);
+}
+
+// ------------------------------------------------------------------ routed side path
+// CTAs per (token, projection): enough to give every SM two CTAs while the batch is small.
+static int mix_cluster(int64_t T, int n_proj) {
+    int cs = 1;
+    while (cs < 8 && T * n_proj * cs < 2 * 148) cs *= 2;
+    return cs;
+}
+
+template <bool GRAD>
+static lf_status launch_mixture_token(const MixArgs& A, cudaStream_t s) {
+    const int cs = mix_cluster(A.T, A.n_proj);
+    constexpr size_t sm = sizeof(MixSmem);
+    LF_CUDA_TRY(cudaFuncSetAttribute(mixture_token_kernel<GRAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)A.T * cs, (unsigned)A.n_proj);
+    cfg.blockDim = dim3(kMixThreads);
+    cfg.dynamicSmemBytes = sm;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cs;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    PhaseScope ps(GRAD ? "mixture_grad" : "mixture", s);
+    LF_CUDA_TRY(cudaLaunchKernelEx(&cfg, mixture_token_kernel<GRAD>, A));
+    return LF_OK;
+}
+
+static lf_status check_mixture(int32_t T, int32_t K, const int32_t* ids, int32_t n_adapters, const void* projs,
+                               int32_t n_proj) {
+    if (T < 0 || n_adapters < 1 || n_adapters > 16384 || n_proj < 1 || n_proj > kMaxProj || !projs)
+        return LF_ERR_INVALID_ARG;
+    if (K < 1 || K > kMixMaxK) return LF_ERR_SHAPE;
+    if ((int64_t)T * 8 > INT_MAX) return LF_ERR_SHAPE;   // grid
+    if (T > 0 && !ids) return LF_ERR_INVALID_ARG;
+    return LF_OK;
+}
+
+static void mix_tables(MixProj& t, const lf_slice& q, int32_t d_in) {
+    t.y_off = q.y_offset;
+    t.d_in = d_in;
+    t.d_out = q.d_out;
+    t.max_rank = q.max_rank;
+    t.ranks = q.ranks;
+    t.off_A = q.off_A;
+    t.off_Bt = q.off_Bt;
+    t.A_pool = reinterpret_cast<const __nv_bfloat16*>(q.A_pool);
+    t.Bt_pool = reinterpret_cast<const __nv_bfloat16*>(q.Bt_pool);
+    t.pool_A = q.pool_elems_A;
+    t.pool_Bt = q.pool_elems_Bt;
+}
+
+static size_t mix_ws_bytes(int64_t T, int K, int n_proj) {   // per-projection weight gradients
+    return n_proj > 1 ? (size_t)T * K * n_proj * sizeof(float) + 256 : 0;
+}
+
+// ------------------------------------------------------------------ 4-bit base weights
+static lf_status check_w4(const void* q, const void* scales, int32_t d_out, int32_t d_in, int32_t group) {
+    if (!q || !scales) return LF_ERR_INVALID_ARG;
+    if (d_in < 1 || (d_in & 31) || d_out < 1 || (group != 32 && group != 64 && group != 128 && group != 256))
+        return LF_ERR_SHAPE;
+    if (!aligned16(q) || (reinterpret_cast<uintptr_t>(scales) & 1) || (d_out & 7)) return LF_ERR_ALIGNMENT;
+    return LF_OK;
+}
+
+static int log2_of(int v) {
+    int l = 0;
+    while ((1 << l) < v) ++l;
+    return l;
+}
+
+template <typename T>
+static cudaError_t launch_w4_quantize(const W4QuantArgs& a, int group, cudaStream_t s) {
+    const int64_t lanes = (int64_t)a.d_out * a.ng * (group / 8);
+    const unsigned grid = (unsigned)cdiv(lanes, 256);
+    switch (group) {
+        case 32: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 32>), grid, 256, 0, s, a); break;
+        case 64: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 64>), grid, 256, 0, s, a); break;
+        case 128: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 128>), grid, 256, 0, s, a); break;
+        default: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 256>), grid, 256, 0, s, a); break;
+    }
+    return cudaGetLastError();
+}
+
+template <int MT, int NT, int DEPTH>
+static lf_status launch_w4_gemv(W4Args& a, cudaStream_t s) {
+    int tiles = 0;
+    for (int p = 0; p < a.n_proj; ++p) {
+        a.p[p].tile0 = tiles;
+        tiles += (int)cdiv(a.p[p].d_out, 16 * MT);
+    }
+    constexpr size_t sm = sizeof(W4Smem<MT, NT, DEPTH>);
+    LF_CUDA_TRY(cudaFuncSetAttribute(w4_gemv_kernel<MT, NT, DEPTH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    LF_LAUNCH("w4_gemv", (w4_gemv_kernel<MT, NT, DEPTH>), dim3((unsigned)tiles, (unsigned)cdiv(a.T, 8 * NT)),
+              32 * kW4Warps, sm, s, a);
+    return launch_status();
+}
+
 }  // namespace lf
+
 
 using namespace lf;
 
@@ -1940,6 +2100,240 @@ const char* lf_status_string(lf_status s) {
         case LF_ERR_ALIGNMENT: return "misaligned pointer, offset or leading dimension";
     }
     return "unknown status";
+}
+
+lf_status lf_route_experts(int32_t T, const lf_router* router, const void* logits, int32_t logits_type,
+                           int64_t logits_ld, const float* bias, int32_t* ids, float* weights, int32_t* counts,
+                           lf_stream_t stream) {
+    const lf_status st = check_router(T, router, logits, logits_type, logits_ld);
+    if (st != LF_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (!aligned4(bias) || !aligned4(ids) || !aligned4(weights) || !aligned4(counts)) return LF_ERR_ALIGNMENT;
+    if (T > 0 && (!ids || !weights)) return LF_ERR_INVALID_ARG;
+    if (counts) LF_CUDA_TRY(cudaMemsetAsync(counts, 0, (size_t)router->n_experts * sizeof(int32_t), s));
+    if (T == 0) return LF_OK;
+    RouterArgs a{};
+    a.logits = logits;
+    a.ld = logits_ld;
+    a.bias = bias;
+    a.T = T;
+    a.E = router->n_experts;
+    a.K = router->top_k;
+    a.G = router->n_groups;
+    a.top_groups = router->top_groups;
+    a.group_top = router->group_top;
+    a.sigmoid = router->score;
+    a.renorm = router->renorm;
+    a.weight_scale = router->weight_scale;
+    a.ids = ids;
+    a.weights = weights;
+    a.counts = counts;
+    LF_CUDA_TRY(launch_router_type(logits_type, a, s));
+    return LF_OK;
+}
+
+lf_status lf_route_experts_backward(int32_t T, const lf_router* router, const void* logits, int32_t logits_type,
+                                    int64_t logits_ld, const int32_t* ids, const float* grad_weights,
+                                    void* grad_logits, int64_t grad_ld, lf_stream_t stream) {
+    const lf_status st = check_router(T, router, logits, logits_type, logits_ld);
+    if (st != LF_OK) return st;
+    if (T == 0) return LF_OK;
+    if (!ids || !grad_weights || !grad_logits || grad_ld < router->n_experts) return LF_ERR_INVALID_ARG;
+    if (!aligned4(ids) || !aligned4(grad_weights) ||
+        reinterpret_cast<uintptr_t>(grad_logits) % (logits_type == LF_F32 ? 4 : 2))
+        return LF_ERR_ALIGNMENT;
+    RouterGradArgs a{};
+    a.logits = logits;
+    a.ld = logits_ld;
+    a.T = T;
+    a.E = router->n_experts;
+    a.K = router->top_k;
+    a.sigmoid = router->score;
+    a.renorm = router->renorm;
+    a.weight_scale = router->weight_scale;
+    a.ids = ids;
+    a.gw = grad_weights;
+    a.dlogits = grad_logits;
+    a.ld_out = grad_ld;
+    LF_CUDA_TRY(launch_router_type(logits_type, a, reinterpret_cast<cudaStream_t>(stream)));
+    return LF_OK;
+}
+
+size_t lf_lora_mixture_workspace_size(int32_t T, int32_t top_k, int32_t n_adapters, int32_t n_proj, int32_t max_rank) {
+    if (T < 0 || top_k < 1 || top_k > kMixMaxK || n_adapters < 1 || n_adapters > 16384 || n_proj < 1 ||
+        n_proj > kMaxProj || max_rank < 0 || max_rank > kMaxRank)
+        return 0;
+    return mix_ws_bytes(T, top_k, n_proj);
+}
+
+lf_status lf_lora_mixture(int32_t T, int32_t top_k, const int32_t* ids, const float* weights, int32_t n_adapters,
+                          const lf_mixture_projection* projs, int32_t n_proj, float scale, const float* adapter_scale,
+                          void* ws, size_t ws_bytes, lf_stream_t stream) {
+    const lf_status st = check_mixture(T, top_k, ids, n_adapters, projs, n_proj);
+    if (st != LF_OK || T == 0) return st;
+    MixArgs A{};
+    A.T = T;
+    A.K = top_k;
+    A.n_adapters = n_adapters;
+    A.n_proj = n_proj;
+    A.ids = ids;
+    A.weights = weights;
+    A.scale = scale;
+    A.scales = adapter_scale;
+    for (int p = 0; p < n_proj; ++p) {
+        const lf_mixture_projection& q = projs[p];
+        if (q.reserved != 0) return LF_ERR_INVALID_ARG;
+        const lf_status cs = check_apply(q.d_in, q.x, q.y, q.y_ld, &q.slice, 1, false);
+        if (cs != LF_OK) return cs;
+        if (q.x_ld < q.d_in) return LF_ERR_INVALID_ARG;
+        if ((q.x_ld & 7) || !aligned16(q.base)) return LF_ERR_ALIGNMENT;
+        MixProj& t = A.p[p];
+        mix_tables(t, q.slice, q.d_in);
+        t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
+        t.in2 = reinterpret_cast<const __nv_bfloat16*>(q.base);
+        t.out = reinterpret_cast<__nv_bfloat16*>(q.y);
+        t.x_ld = q.x_ld;
+        t.out_ld = q.y_ld;
+    }
+    (void)ws;
+    (void)ws_bytes;
+    return launch_mixture_token<false>(A, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids, const float* weights,
+                                   int32_t n_adapters, const lf_mixture_grad* projs, int32_t n_proj, float scale,
+                                   const float* adapter_scale, float* grad_weights, void* ws, size_t ws_bytes,
+                                   lf_stream_t stream) {
+    const lf_status st = check_mixture(T, top_k, ids, n_adapters, projs, n_proj);
+    if (st != LF_OK || T == 0) return st;
+    MixArgs A{};
+    A.T = T;
+    A.K = top_k;
+    A.n_adapters = n_adapters;
+    A.n_proj = n_proj;
+    A.ids = ids;
+    A.weights = weights;
+    A.scale = scale;
+    A.scales = adapter_scale;
+    bool any = grad_weights != nullptr;
+    for (int p = 0; p < n_proj; ++p) {
+        const lf_mixture_grad& q = projs[p];
+        if (q.reserved != 0) return LF_ERR_INVALID_ARG;
+        const lf_status cs = check_apply(q.d_in, q.x, q.dy, q.dy_ld, &q.slice, 1, false);
+        if (cs != LF_OK) return cs;
+        if (q.x_ld < q.d_in || (q.dx && q.dx_ld < q.d_in) || (q.dx_base && !q.dx)) return LF_ERR_INVALID_ARG;
+        if ((q.x_ld & 7) || (q.dx && (q.dx_ld & 7)) || !aligned16(q.dx) || !aligned16(q.dx_base)) return LF_ERR_ALIGNMENT;
+        any = any || q.dx;
+        MixProj& t = A.p[p];
+        mix_tables(t, q.slice, q.d_in);
+        t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
+        t.in2 = reinterpret_cast<const __nv_bfloat16*>(q.dy);
+        t.base = reinterpret_cast<const __nv_bfloat16*>(q.dx_base);
+        t.out = reinterpret_cast<__nv_bfloat16*>(q.dx);
+        t.x_ld = q.x_ld;
+        t.dy_ld = q.dy_ld;
+        t.out_ld = q.dx_ld;
+    }
+    if (!any) return LF_OK;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool sum = grad_weights && n_proj > 1;
+    if (sum) {
+        if (!ws) return LF_ERR_INVALID_ARG;
+        if (ws_bytes < mix_ws_bytes(T, top_k, n_proj)) return LF_ERR_WORKSPACE;
+        A.gw = reinterpret_cast<float*>(align_up((int64_t)reinterpret_cast<uintptr_t>(ws), 256));
+    } else {
+        A.gw = grad_weights;
+    }
+    const lf_status ls = launch_mixture_token<true>(A, s);
+    if (ls != LF_OK || !sum) return ls;
+    const int64_t n = (int64_t)T * top_k;
+    LF_LAUNCH("mixture_gw_sum", mixture_gw_sum_kernel, (unsigned)cdiv(n, 256), 256, 0, s, A.gw, n_proj, n, grad_weights);
+    return launch_status();
+}
+
+lf_status lf_w4_quantize(const void* W, int32_t W_type, int32_t d_out, int32_t d_in, int32_t group, void* q,
+                         void* scales, void* zeros, lf_stream_t stream) {
+    if (!W || W_type < LF_F32 || W_type > LF_F16) return LF_ERR_INVALID_ARG;
+    const lf_status st = check_w4(q, scales, d_out, d_in, group);
+    if (st != LF_OK) return st;
+    if (!aligned16(W)) return LF_ERR_ALIGNMENT;
+    W4QuantArgs a{W, d_out, d_in, (int32_t)cdiv(d_in, group), reinterpret_cast<uint8_t*>(q),
+                  reinterpret_cast<__nv_bfloat16*>(scales), reinterpret_cast<uint8_t*>(zeros)};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (W_type == LF_F32) LF_CUDA_TRY(launch_w4_quantize<float>(a, group, s));
+    else if (W_type == LF_BF16) LF_CUDA_TRY(launch_w4_quantize<__nv_bfloat16>(a, group, s));
+    else LF_CUDA_TRY(launch_w4_quantize<__half>(a, group, s));
+    return LF_OK;
+}
+
+lf_status lf_w4_dequantize(const void* q, const void* scales, const void* zeros, int32_t d_out, int32_t d_in,
+                           int32_t group, void* W, int32_t W_type, lf_stream_t stream) {
+    if (!W || W_type < LF_F32 || W_type > LF_F16) return LF_ERR_INVALID_ARG;
+    const lf_status st = check_w4(q, scales, d_out, d_in, group);
+    if (st != LF_OK) return st;
+    if (!aligned16(W)) return LF_ERR_ALIGNMENT;
+    W4DequantArgs a{reinterpret_cast<const uint8_t*>(q), reinterpret_cast<const __nv_bfloat16*>(scales),
+                    reinterpret_cast<const uint8_t*>(zeros), d_out, d_in, (int32_t)cdiv(d_in, group), log2_of(group), W};
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const unsigned grid = (unsigned)cdiv((int64_t)d_out * (d_in / 8), 256);
+    if (W_type == LF_F32) LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<float>, grid, 256, 0, s, a);
+    else if (W_type == LF_BF16) LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<__nv_bfloat16>, grid, 256, 0, s, a);
+    else LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<__half>, grid, 256, 0, s, a);
+    return launch_status();
+}
+
+size_t lf_w4_workspace_size(int32_t T, const lf_w4_projection* projs, int32_t n_proj) {
+    (void)T;
+    (void)projs;
+    (void)n_proj;
+    return 0;
+}
+
+static_assert(kW4MaxProj == LF_MAX_PROJECTIONS, "projection table size");
+
+lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_proj, void* ws, size_t ws_bytes,
+                            lf_stream_t stream) {
+    if (T < 0 || n_proj < 1 || n_proj > LF_MAX_PROJECTIONS || !projs) return LF_ERR_INVALID_ARG;
+    W4Args a{};
+    a.T = T;
+    a.n_proj = n_proj;
+    int64_t rows = 0;
+    for (int p = 0; p < n_proj; ++p) {
+        const lf_w4_projection& q = projs[p];
+        if (T > 0 && (!q.x || !q.y)) return LF_ERR_INVALID_ARG;
+        const lf_status st = check_w4(q.q, q.scales, q.d_out, q.d_in, q.group);
+        if (st != LF_OK) return st;
+        if (q.x_ld < q.d_in || q.y_ld < q.d_out || q.reserved != 0) return LF_ERR_INVALID_ARG;
+        if (!aligned16(q.x) || !aligned16(q.y) || (q.x_ld & 7) || (q.y_ld & 7) || (reinterpret_cast<uintptr_t>(q.bias) & 1))
+            return LF_ERR_ALIGNMENT;
+        rows += q.d_out;
+    }
+    if (T == 0) return LF_OK;
+    // the longest rows first, so that their CTAs start in the first wave
+    int order[LF_MAX_PROJECTIONS];
+    for (int p = 0; p < n_proj; ++p) order[p] = p;
+    std::stable_sort(order, order + n_proj, [&](int u, int v) { return projs[u].d_in > projs[v].d_in; });
+    for (int i = 0; i < n_proj; ++i) {
+        const lf_w4_projection& q = projs[order[i]];
+        W4Proj& t = a.p[i];
+        t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
+        t.y = reinterpret_cast<__nv_bfloat16*>(q.y);
+        t.q = reinterpret_cast<const uint8_t*>(q.q);
+        t.scales = reinterpret_cast<const __nv_bfloat16*>(q.scales);
+        t.zeros = reinterpret_cast<const uint8_t*>(q.zeros);
+        t.bias = reinterpret_cast<const __nv_bfloat16*>(q.bias);
+        t.x_ld = q.x_ld;
+        t.y_ld = q.y_ld;
+        t.d_in = q.d_in;
+        t.d_out = q.d_out;
+        t.ng = (int32_t)cdiv(q.d_in, q.group);
+        t.log_u = log2_of(q.group / 32);
+    }
+    (void)ws;
+    (void)ws_bytes;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (T <= 8) return rows <= 148 * 32 ? launch_w4_gemv<1, 1, 4>(a, s) : launch_w4_gemv<2, 1, 4>(a, s);
+    return rows <= 148 * 32 ? launch_w4_gemv<1, 2, 4>(a, s) : launch_w4_gemv<2, 2, 4>(a, s);
 }
 
 lf_status lf_check_bounded_wait(int32_t polls, lf_stream_t stream) {

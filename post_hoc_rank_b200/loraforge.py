@@ -75,6 +75,49 @@ class lf_projection(ctypes.Structure):
 MAX_PROJECTIONS = 8
 
 
+class lf_router(ctypes.Structure):
+    """Routing of tokens to experts (mirrors the C struct; make_router)."""
+    _fields_ = [("n_experts", ctypes.c_int32), ("top_k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("n_groups", ctypes.c_int32), ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("weight_scale", ctypes.c_float)]
+
+
+class lf_mixture_projection(ctypes.Structure):
+    """One projection of lf_lora_mixture (mirrors the C struct)."""
+    _fields_ = [("x", ctypes.c_void_p), ("base", ctypes.c_void_p), ("y", ctypes.c_void_p), ("d_in", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("x_ld", ctypes.c_int64), ("y_ld", ctypes.c_int64), ("slice", lf_slice)]
+
+
+class lf_mixture_grad(ctypes.Structure):
+    """One projection of lf_lora_mixture_backward (mirrors the C struct)."""
+    _fields_ = [("x", ctypes.c_void_p), ("dy", ctypes.c_void_p), ("dx_base", ctypes.c_void_p), ("dx", ctypes.c_void_p),
+                ("d_in", ctypes.c_int32), ("reserved", ctypes.c_int32), ("x_ld", ctypes.c_int64),
+                ("dy_ld", ctypes.c_int64), ("dx_ld", ctypes.c_int64), ("slice", lf_slice)]
+
+
+class lf_w4_projection(ctypes.Structure):
+    """One projection of lf_w4_projections (mirrors the C struct)."""
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("q", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("zeros", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("d_in", ctypes.c_int32),
+                ("d_out", ctypes.c_int32), ("group", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("x_ld", ctypes.c_int64), ("y_ld", ctypes.c_int64)]
+
+
+ROUTER_MAX_EXPERTS = 1024
+ROUTER_MAX_K = 16
+# element types of logits and weight matrices
+LF_F32, LF_BF16, LF_F16 = 0, 1, 2
+_TYPE_CODES = {"torch.float32": LF_F32, "torch.bfloat16": LF_BF16, "torch.float16": LF_F16}
+
+
+def type_code(dtype) -> int:
+    """LF_F32 / LF_BF16 / LF_F16 of a torch dtype."""
+    try:
+        return _TYPE_CODES[str(dtype)]
+    except KeyError:
+        raise ValueError(f"float32, bfloat16 or float16 expected, got {dtype}") from None
+
+
 class LFError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -136,6 +179,21 @@ def lib() -> ctypes.CDLL:
         L.lf_pool_workspace_size.argtypes = [_I32, _I32, _P, _P, _I32]; L.lf_pool_workspace_size.restype = _SZ
         L.lf_pool_subspace.argtypes = [_I32, _I32, _P, _P, _I32, _P, _I32, _I32, _P, _P, _P, _P, _P, _P, _SZ, _P]
         L.lf_pool_subspace.restype = ctypes.c_int
+        _F = ctypes.c_float
+        L.lf_route_experts.argtypes = [_I32, _P, _P, _I32, _I64, _P, _P, _P, _P, _P]
+        L.lf_route_experts.restype = ctypes.c_int
+        L.lf_route_experts_backward.argtypes = [_I32, _P, _P, _I32, _I64, _P, _P, _P, _I64, _P]
+        L.lf_route_experts_backward.restype = ctypes.c_int
+        L.lf_lora_mixture_workspace_size.argtypes = [_I32] * 5; L.lf_lora_mixture_workspace_size.restype = _SZ
+        L.lf_lora_mixture.argtypes = [_I32, _I32, _P, _P, _I32, _P, _I32, _F, _P, _P, _SZ, _P]
+        L.lf_lora_mixture.restype = ctypes.c_int
+        L.lf_lora_mixture_backward.argtypes = [_I32, _I32, _P, _P, _I32, _P, _I32, _F, _P, _P, _P, _SZ, _P]
+        L.lf_lora_mixture_backward.restype = ctypes.c_int
+        L.lf_w4_quantize.argtypes = [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P]; L.lf_w4_quantize.restype = ctypes.c_int
+        L.lf_w4_dequantize.argtypes = [_P, _P, _P, _I32, _I32, _I32, _P, _I32, _P]
+        L.lf_w4_dequantize.restype = ctypes.c_int
+        L.lf_w4_workspace_size.argtypes = [_I32, _P, _I32]; L.lf_w4_workspace_size.restype = _SZ
+        L.lf_w4_projections.argtypes = [_I32, _P, _I32, _P, _SZ, _P]; L.lf_w4_projections.restype = ctypes.c_int
         L.lf_status_string.argtypes = [ctypes.c_int]; L.lf_status_string.restype = ctypes.c_char_p
         L.lf_get_device_status.argtypes = [_P]; L.lf_get_device_status.restype = ctypes.c_int
         L.lf_profile_enable.argtypes = [ctypes.c_int]; L.lf_profile_enable.restype = None
@@ -154,7 +212,9 @@ def exported_symbols() -> list[str]:
             "lf_lora_shrink_expand_noalloc", "lf_apply_slices_workspace_size", "lf_lora_shrink_expand_slices",
             "lf_lora_sigma_sandwich", "lf_jd_workspace_size", "lf_jd_full", "lf_route_tokens",
             "lf_lora_shrink_expand_slices_routed", "lf_check_bounded_wait", "lf_pool_workspace_size",
-            "lf_pool_subspace", "lf_lora_shrink_expand_projections"]
+            "lf_pool_subspace", "lf_lora_shrink_expand_projections", "lf_route_experts", "lf_route_experts_backward",
+            "lf_lora_mixture_workspace_size", "lf_lora_mixture", "lf_lora_mixture_backward", "lf_w4_quantize",
+            "lf_w4_dequantize", "lf_w4_workspace_size", "lf_w4_projections"]
 
 # Limits of lf_lora_shrink_expand_noalloc (its scratch is a fixed array in the library).
 NOALLOC_MAX_TOKENS = 16384
@@ -325,6 +385,140 @@ def lf_lora_sigma_sandwich(x, y, ids, n_adapters, Vt, Ut, sigma, diagonal, scale
                                       _ptr(Vt), _ptr(Ut), _ptr(sigma), 1 if diagonal else 0, float(scale), _ptr(ws),
                                       ws.numel() if ws is not None else 0, _stream(stream))
     return _check(st, "lf_lora_sigma_sandwich") if check else st
+
+
+def _row_stride(t, what: str) -> int:
+    """Row stride of a 2-D bf16 tensor whose columns lie side by side."""
+    if t.dim() != 2 or str(t.dtype) != "torch.bfloat16" or (t.shape[0] > 0 and t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: a 2-D bfloat16 tensor with unit column stride expected")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def make_router(n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, top_groups: int = 1,
+                group_top: int = 1, renorm: bool = True, weight_scale: float = 1.0) -> lf_router:
+    """lf_router; score "softmax" or "sigmoid"."""
+    codes = {"softmax": 0, "sigmoid": 1}
+    if score not in codes:
+        raise ValueError(f"score must be softmax or sigmoid, got {score!r}")
+    return lf_router(int(n_experts), int(top_k), codes[score], int(n_groups), int(top_groups), int(group_top),
+                     1 if renorm else 0, float(weight_scale))
+
+
+def _logits_ld(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def lf_route_experts(logits, router: lf_router, bias, ids, weights, counts=None, stream=None, check=True) -> int:
+    """Routing of T tokens (logits: T rows of fp32, bf16 or fp16, unit column stride): ids T x top_k
+    int32, weights T x top_k fp32, counts (nullable) n_experts int32."""
+    st = lib().lf_route_experts(logits.shape[0], ctypes.byref(router), _ptr(logits), type_code(logits.dtype),
+                                _logits_ld(logits), _ptr(bias), _ptr(ids), _ptr(weights), _ptr(counts), _stream(stream))
+    return _check(st, "lf_route_experts") if check else st
+
+
+def lf_route_experts_backward(logits, router: lf_router, ids, grad_weights, grad_logits, stream=None,
+                              check=True) -> int:
+    """grad_logits (the logits' type, unit column stride) from grad_weights at the forward's ids."""
+    st = lib().lf_route_experts_backward(logits.shape[0], ctypes.byref(router), _ptr(logits), type_code(logits.dtype),
+                                         _logits_ld(logits), _ptr(ids), _ptr(grad_weights), _ptr(grad_logits),
+                                         _logits_ld(grad_logits), _stream(stream))
+    return _check(st, "lf_route_experts_backward") if check else st
+
+
+def make_mixture_projection(x, y, sl: lf_slice, base=None) -> lf_mixture_projection:
+    """lf_mixture_projection from device tensors: x T x d_in bf16, y T x y_ld bf16 (rows may be
+    strided), base None (zeros) or laid out like y (y itself: in place)."""
+    y_ld = _row_stride(y, "y")
+    if base is not None and (_row_stride(base, "base") != y_ld or base.shape != y.shape):
+        raise ValueError("base must have y's shape and row stride")
+    if x.shape[0] != y.shape[0]:
+        raise ValueError("x and y must have the same rows")
+    p = lf_mixture_projection(_ptr(x), _ptr(base), _ptr(y), int(x.shape[1]), 0, _row_stride(x, "x"), y_ld, sl)
+    p.rows = int(x.shape[0])
+    return p
+
+
+def make_mixture_grad(x, dy, dx, sl: lf_slice, dx_base=None) -> lf_mixture_grad:
+    """lf_mixture_grad from device tensors: x and dx T x d_in, dy T x dy_ld (bf16, rows may be
+    strided); dx None = not wanted, dx_base None (zeros) or laid out like dx."""
+    dx_ld = _row_stride(dx, "dx") if dx is not None else 0
+    if dx is not None and dx.shape != x.shape:
+        raise ValueError("dx must have x's shape")
+    if dx_base is not None and (dx is None or _row_stride(dx_base, "dx_base") != dx_ld or dx_base.shape != dx.shape):
+        raise ValueError("dx_base must have dx's shape and row stride")
+    if x.shape[0] != dy.shape[0]:
+        raise ValueError("x and dy must have the same rows")
+    p = lf_mixture_grad(_ptr(x), _ptr(dy), _ptr(dx_base), _ptr(dx), int(x.shape[1]), 0, _row_stride(x, "x"),
+                        _row_stride(dy, "dy"), dx_ld, sl)
+    p.rows = int(x.shape[0])
+    return p
+
+
+def lf_lora_mixture_workspace_size(T: int, top_k: int, n_adapters: int, n_proj: int, max_rank: int = 0) -> int:
+    return lib().lf_lora_mixture_workspace_size(T, top_k, n_adapters, n_proj, max_rank)
+
+
+def lf_lora_mixture(ids, weights, n_adapters, projections, scale, ws=None, adapter_scale=None, stream=None,
+                    check=True) -> int:
+    """Routed side path: ids T x top_k int32, weights T x top_k fp32 or None, up to MAX_PROJECTIONS
+    projections (make_mixture_projection)."""
+    T, K = ids.shape
+    arr = (lf_mixture_projection * len(projections))(*projections)
+    st = lib().lf_lora_mixture(T, K, _ptr(ids), _ptr(weights), n_adapters, arr, len(projections), float(scale),
+                               _ptr(adapter_scale), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream))
+    return _check(st, "lf_lora_mixture") if check else st
+
+
+def lf_lora_mixture_backward(ids, weights, n_adapters, grads, scale, grad_weights=None, ws=None, adapter_scale=None,
+                             stream=None, check=True) -> int:
+    """Gradients of lf_lora_mixture for x (per projection, make_mixture_grad) and the weights."""
+    T, K = ids.shape
+    arr = (lf_mixture_grad * len(grads))(*grads)
+    st = lib().lf_lora_mixture_backward(T, K, _ptr(ids), _ptr(weights), n_adapters, arr, len(grads), float(scale),
+                                        _ptr(adapter_scale), _ptr(grad_weights), _ptr(ws),
+                                        ws.numel() if ws is not None else 0, _stream(stream))
+    return _check(st, "lf_lora_mixture_backward") if check else st
+
+
+def lf_w4_quantize(W, group: int, q, scales, zeros=None, stream=None, check=True) -> int:
+    """4-bit codes q (d_out x d_in / 2 uint8), scales (d_out x ng bf16) and, unless None, zero
+    points (d_out x ng uint8) of W (d_out x d_in fp32, bf16 or fp16)."""
+    d_out, d_in = W.shape
+    st = lib().lf_w4_quantize(_ptr(W), type_code(W.dtype), d_out, d_in, int(group), _ptr(q), _ptr(scales), _ptr(zeros),
+                              _stream(stream))
+    return _check(st, "lf_w4_quantize") if check else st
+
+
+def lf_w4_dequantize(q, scales, zeros, group: int, W, stream=None, check=True) -> int:
+    """W (d_out x d_in fp32, bf16 or fp16) = (q - zeros) * scales."""
+    d_out, d_in = W.shape
+    st = lib().lf_w4_dequantize(_ptr(q), _ptr(scales), _ptr(zeros), d_out, d_in, int(group), _ptr(W),
+                                type_code(W.dtype), _stream(stream))
+    return _check(st, "lf_w4_dequantize") if check else st
+
+
+def make_w4_projection(x, y, q, scales, group: int, zeros=None, bias=None) -> lf_w4_projection:
+    """lf_w4_projection from device tensors: x T x d_in and y T x d_out bf16 (rows may be strided),
+    the 4-bit weights as lf_w4_quantize lays them out, bias d_out bf16 or None."""
+    if x.shape[0] != y.shape[0] or x.shape[1] != 2 * q.shape[1] or y.shape[1] < q.shape[0]:
+        raise ValueError(f"shapes do not fit: x {tuple(x.shape)}, y {tuple(y.shape)}, q {tuple(q.shape)}")
+    p = lf_w4_projection(_ptr(x), _ptr(y), _ptr(q), _ptr(scales), _ptr(zeros), _ptr(bias), int(x.shape[1]),
+                         int(q.shape[0]), int(group), 0, _row_stride(x, "x"), _row_stride(y, "y"))
+    p.rows, p.device = int(x.shape[0]), x.device
+    return p
+
+
+def lf_w4_workspace_size(T: int, projections) -> int:
+    arr = (lf_w4_projection * len(projections))(*projections)
+    return lib().lf_w4_workspace_size(int(T), arr, len(projections))
+
+
+def lf_w4_projections(T: int, projections, ws=None, stream=None, check=True) -> int:
+    """y = x W0^T + bias for up to MAX_PROJECTIONS projections (make_w4_projection) of T tokens."""
+    arr = (lf_w4_projection * len(projections))(*projections)
+    st = lib().lf_w4_projections(int(T), arr, len(projections), _ptr(ws), ws.numel() if ws is not None else 0,
+                                 _stream(stream))
+    return _check(st, "lf_w4_projections") if check else st
 
 
 def _jd_tables(mods, members, probs):
