@@ -1112,30 +1112,47 @@ static int log2_of(int v) {
     return l;
 }
 
+// threads of a row-wise kernel: 8 columns each, whole warps
+static int w4_row_threads(int d_in) { return (int)std::min<int64_t>(256, align_up(d_in / 8, 32)); }
+
 template <typename T>
 static cudaError_t launch_w4_quantize(const W4QuantArgs& a, int group, cudaStream_t s) {
-    const int64_t lanes = (int64_t)a.d_out * a.ng * (group / 8);
-    const unsigned grid = (unsigned)cdiv(lanes, 256);
+    const unsigned grid = (unsigned)a.d_out;
+    const int thr = w4_row_threads(a.d_in);
     switch (group) {
-        case 32: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 32>), grid, 256, 0, s, a); break;
-        case 64: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 64>), grid, 256, 0, s, a); break;
-        case 128: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 128>), grid, 256, 0, s, a); break;
-        default: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 256>), grid, 256, 0, s, a); break;
+        case 32: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 32>), grid, thr, 0, s, a); break;
+        case 64: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 64>), grid, thr, 0, s, a); break;
+        case 128: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 128>), grid, thr, 0, s, a); break;
+        default: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 256>), grid, thr, 0, s, a); break;
     }
     return cudaGetLastError();
 }
 
-template <int MT, int NT, int DEPTH>
-static lf_status launch_w4_gemv(W4Args& a, cudaStream_t s) {
+// Tensor map of 4-bit codes (d_out rows of d_in / 2 bytes): box of 128 bytes x `rows` rows,
+// 128-byte swizzle, what lies outside reads as zeros.
+static bool encode_q_map(CUtensorMap* map, const void* q, int32_t d_out, int32_t d_in, int rows) {
+    const EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d_in / 2, (cuuint64_t)d_out};
+    const cuuint64_t strides[1] = {(cuuint64_t)d_in / 2};
+    const cuuint32_t box[2] = {128u, (cuuint32_t)rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT, bool WIDE>
+static lf_status launch_w4_gemv(W4Args& a, const W4Maps& maps, cudaStream_t s) {
     int tiles = 0;
     for (int p = 0; p < a.n_proj; ++p) {
         a.p[p].tile0 = tiles;
-        tiles += (int)cdiv(a.p[p].d_out, 16 * MT);
+        tiles += (int)cdiv(a.p[p].d_out, kW4Rows);
     }
-    constexpr size_t sm = sizeof(W4Smem<MT, NT, DEPTH>);
-    LF_CUDA_TRY(cudaFuncSetAttribute(w4_gemv_kernel<MT, NT, DEPTH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
-    LF_LAUNCH("w4_gemv", (w4_gemv_kernel<MT, NT, DEPTH>), dim3((unsigned)tiles, (unsigned)cdiv(a.T, 8 * NT)),
-              32 * kW4Warps, sm, s, a);
+    constexpr size_t sm = sizeof(W4Smem<NT>);
+    LF_CUDA_TRY(cudaFuncSetAttribute(w4_gemv_kernel<NT, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    LF_LAUNCH("w4_gemv", (w4_gemv_kernel<NT, WIDE>), dim3((unsigned)tiles, (unsigned)cdiv(a.T, 8 * NT)), 32 * kW4Warps,
+              sm, s, a, maps);
     return launch_status();
 }
 
@@ -2122,6 +2139,7 @@ lf_status lf_route_experts(int32_t T, const lf_router* router, const void* logit
     a.G = router->n_groups;
     a.top_groups = router->top_groups;
     a.group_top = router->group_top;
+    a.group_mul = (int32_t)cdiv(1 << 20, router->n_experts / router->n_groups);
     a.sigmoid = router->score;
     a.renorm = router->renorm;
     a.weight_scale = router->weight_scale;
@@ -2275,10 +2293,11 @@ lf_status lf_w4_dequantize(const void* q, const void* scales, const void* zeros,
     W4DequantArgs a{reinterpret_cast<const uint8_t*>(q), reinterpret_cast<const __nv_bfloat16*>(scales),
                     reinterpret_cast<const uint8_t*>(zeros), d_out, d_in, (int32_t)cdiv(d_in, group), log2_of(group), W};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)cdiv((int64_t)d_out * (d_in / 8), 256);
-    if (W_type == LF_F32) LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<float>, grid, 256, 0, s, a);
-    else if (W_type == LF_BF16) LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<__nv_bfloat16>, grid, 256, 0, s, a);
-    else LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<__half>, grid, 256, 0, s, a);
+    const unsigned grid = (unsigned)d_out;
+    const int thr = w4_row_threads(d_in);
+    if (W_type == LF_F32) LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<float>, grid, thr, 0, s, a);
+    else if (W_type == LF_BF16) LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<__nv_bfloat16>, grid, thr, 0, s, a);
+    else LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<__half>, grid, thr, 0, s, a);
     return launch_status();
 }
 
@@ -2297,7 +2316,6 @@ lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_
     W4Args a{};
     a.T = T;
     a.n_proj = n_proj;
-    int64_t rows = 0;
     for (int p = 0; p < n_proj; ++p) {
         const lf_w4_projection& q = projs[p];
         if (T > 0 && (!q.x || !q.y)) return LF_ERR_INVALID_ARG;
@@ -2306,19 +2324,22 @@ lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_
         if (q.x_ld < q.d_in || q.y_ld < q.d_out || q.reserved != 0) return LF_ERR_INVALID_ARG;
         if (!aligned16(q.x) || !aligned16(q.y) || (q.x_ld & 7) || (q.y_ld & 7) || (reinterpret_cast<uintptr_t>(q.bias) & 1))
             return LF_ERR_ALIGNMENT;
-        rows += q.d_out;
     }
     if (T == 0) return LF_OK;
     // the longest rows first, so that their CTAs start in the first wave
     int order[LF_MAX_PROJECTIONS];
     for (int p = 0; p < n_proj; ++p) order[p] = p;
     std::stable_sort(order, order + n_proj, [&](int u, int v) { return projs[u].d_in > projs[v].d_in; });
+    W4Maps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    bool wide = true;   // every group holds whole 128-column pieces
     for (int i = 0; i < n_proj; ++i) {
         const lf_w4_projection& q = projs[order[i]];
         W4Proj& t = a.p[i];
         t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
         t.y = reinterpret_cast<__nv_bfloat16*>(q.y);
-        t.q = reinterpret_cast<const uint8_t*>(q.q);
+        if (!encode_q_map(&maps.q[i], q.q, q.d_out, q.d_in, kW4Rows)) return LF_ERR_CUDA;
+        wide = wide && q.group >= 128;
         t.scales = reinterpret_cast<const __nv_bfloat16*>(q.scales);
         t.zeros = reinterpret_cast<const uint8_t*>(q.zeros);
         t.bias = reinterpret_cast<const __nv_bfloat16*>(q.bias);
@@ -2332,8 +2353,8 @@ lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_
     (void)ws;
     (void)ws_bytes;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (T <= 8) return rows <= 148 * 32 ? launch_w4_gemv<1, 1, 4>(a, s) : launch_w4_gemv<2, 1, 4>(a, s);
-    return rows <= 148 * 32 ? launch_w4_gemv<1, 2, 4>(a, s) : launch_w4_gemv<2, 2, 4>(a, s);
+    if (T <= 8) return wide ? launch_w4_gemv<1, true>(a, maps, s) : launch_w4_gemv<1, false>(a, maps, s);
+    return wide ? launch_w4_gemv<2, true>(a, maps, s) : launch_w4_gemv<2, false>(a, maps, s);
 }
 
 lf_status lf_check_bounded_wait(int32_t polls, lf_stream_t stream) {

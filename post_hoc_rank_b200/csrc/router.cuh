@@ -30,6 +30,7 @@ struct RouterArgs {
     int64_t ld;
     const float* bias;      // nullable, E
     int32_t T, E, K, G, top_groups, group_top;
+    int32_t group_mul;      // e / (E / G) = e * group_mul >> 20 for e < 1024
     int32_t sigmoid, renorm;
     float weight_scale;
     int32_t* ids;           // T x K
@@ -77,6 +78,12 @@ __device__ __forceinline__ double warp_max(double v) {
     return v;
 }
 
+// For the choice alone (its rounding is allowed for): hardware exponential and reciprocal.
+__device__ __forceinline__ float fast_sigmoid(float l) {
+    const float e = __expf(-fabsf(l));
+    return __fdividef(l >= 0.f ? 1.f : e, 1.f + e);
+}
+
 __device__ __forceinline__ float sigmoid_f32(float l) {   // no overflow on either side
     const float e = expf(-fabsf(l));
     return (l >= 0.f ? 1.f : e) / (1.f + e);
@@ -90,26 +97,27 @@ template <typename TL>
 __device__ __noinline__ int route_row_f64(const RouterArgs& a, const TL* row, double* c) {
     const int lane = threadIdx.x & 31;
     double m = -INFINITY;
-    for (int e = lane; e < a.E; e += 32) {
-        m = fmax(m, (double)to_f32(row[e]));   // a bias shuts an expert out of the choice, not of the scores
-    }
-    m = warp_max(m);
-    double denom = 1.0;
+    for (int e = lane; e < a.E; e += 32) m = fmax(m, (double)to_f32(row[e]));
+    m = warp_max(m);   // a bias shuts an expert out of the choice, not of the scores
+    double inv = 1.0;
     if (!a.sigmoid) {
         double s = 0.0;
-        for (int e = lane; e < a.E; e += 32) s += m == -INFINITY ? 0.0 : exp((double)to_f32(row[e]) - m);
-        denom = warp_sum(s);
+        for (int e = lane; e < a.E; e += 32) {
+            const double p = m == -INFINITY ? 0.0 : exp((double)to_f32(row[e]) - m);
+            c[e] = p;
+            s += p;
+        }
+        inv = warp_sum(s);
     }
     for (int e = lane; e < a.E; e += 32) {
         const float l = to_f32(row[e]);
         const float b = a.bias ? a.bias[e] : 0.f;
-        const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - m) / denom;
+        const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : c[e] / inv;
         c[e] = l == -INFINITY || b == -INFINITY ? -INFINITY : s + (double)b;
     }
     __syncwarp();
-    uint32_t kept = 0xffffffffu;   // groups that stay
-    const int n = a.E / a.G;
     if (a.G > 1) {
+        const int n = a.E / a.G;
         double mine = -INFINITY;   // group `lane`
         for (int g = 0; g < a.G; ++g) {
             double b1 = -INFINITY, b2 = -INFINITY;
@@ -130,33 +138,45 @@ __device__ __noinline__ int route_row_f64(const RouterArgs& a, const TL* row, do
             const double o = __shfl_sync(0xffffffffu, mine, g);
             rank += o > mine || (o == mine && g < lane);
         }
-        kept = __ballot_sync(0xffffffffu, lane < a.G && mine > -INFINITY && rank < a.top_groups);
+        const uint32_t kept = __ballot_sync(0xffffffffu, lane < a.G && mine > -INFINITY && rank < a.top_groups);
+        for (int g = 0; g < a.G; ++g)
+            if (!((kept >> g) & 1u))
+                for (int e = g * n + lane; e < (g + 1) * n; e += 32) c[e] = -INFINITY;
+        __syncwarp();
     }
-    uint32_t taken = 0;   // bit i: expert 32 i + lane
-    int chosen = -1;
+    if (!a.bias) {   // the logit decides among those that are left
+        for (int e = lane; e < a.E; e += 32)
+            if (c[e] > -INFINITY) c[e] = to_f32(row[e]);
+        __syncwarp();
+    }
+    int chosen = -1, last = -1;
+    double best = -INFINITY;
+    int at = INT_MAX;
     for (int j = 0; j < a.K; ++j) {
-        double best = -INFINITY;
-        int at = INT_MAX;
-        for (int i = 0, e = lane; e < a.E; ++i, e += 32) {
-            if (((taken >> i) & 1u) || c[e] == -INFINITY || !((kept >> (e / n)) & 1u)) continue;
-            const double v = a.bias ? c[e] : (double)to_f32(row[e]);
-            if (at == INT_MAX || v > best) {
-                best = v;
-                at = e;
-            }
+        if (last < 0 || (last & 31) == lane) {   // this lane's best has changed
+            best = -INFINITY;
+            at = INT_MAX;
+            for (int e = lane; e < a.E; e += 32)
+                if (c[e] > best) {
+                    best = c[e];
+                    at = e;
+                }
         }
+        double tv = best;
+        int te = at;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            const double ov = __shfl_xor_sync(0xffffffffu, best, o);
-            const int oe = __shfl_xor_sync(0xffffffffu, at, o);
-            if (oe != INT_MAX && (at == INT_MAX || ov > best || (ov == best && oe < at))) {
-                best = ov;
-                at = oe;
+            const double ov = __shfl_xor_sync(0xffffffffu, tv, o);
+            const int oe = __shfl_xor_sync(0xffffffffu, te, o);
+            if (ov > tv || (ov == tv && oe < te)) {
+                tv = ov;
+                te = oe;
             }
         }
-        if (at == INT_MAX) break;   // uniform
-        if ((at & 31) == lane) taken |= 1u << (at >> 5);
-        if (lane == j) chosen = at;
+        if (te == INT_MAX) break;   // uniform
+        last = te;
+        if ((te & 31) == lane) c[te] = -INFINITY;
+        if (lane == j) chosen = te;
     }
     return chosen;
 }
@@ -198,27 +218,32 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_experts_kernel(Router
     float bmax = 0.f;
     uint32_t key[EPL];   // order image of what chooses; 0 = not to be chosen
     const bool scores = a.bias != nullptr || (a.G > 1 && a.group_top == 2);
-    float denom = 1.f;
     m = warp_max(m);
-    if (!a.sigmoid && (scores || !a.renorm)) {   // the softmax's denominator
+    float c[EPL];        // selection score (only with `scores`)
+    float rden = 1.f;    // 1 / softmax denominator, for the choice
+    if (scores && !a.sigmoid) {
         float s = 0.f;
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) s += l[i] == -INFINITY ? 0.f : expf(l[i] - m);
-        denom = warp_sum(s);
+        for (int i = 0; i < EPL; ++i) {
+            c[i] = l[i] == -INFINITY ? 0.f : __expf(l[i] - m);
+            s += c[i];
+        }
+        s = warp_sum(s);
+        rden = s > 0.f ? __fdividef(1.f, s) : 0.f;
     }
-    float c[EPL];        // selection score (only with `scores`)
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
         const int e = 32 * i + lane;
         float b = 0.f;
-        c[i] = 0.f;
         if (scores) {
             if (a.bias && e < E) {
                 b = a.bias[e];
                 bad = bad || !(b < INFINITY);
                 if (b != -INFINITY) bmax = fmaxf(bmax, fabsf(b));
             }
-            c[i] = (a.sigmoid ? sigmoid_f32(l[i]) : expf(l[i] - m) / denom) + b;
+            c[i] = (a.sigmoid ? fast_sigmoid(l[i]) : c[i] * rden) + b;
+        } else {
+            c[i] = 0.f;
         }
         const bool open = l[i] != -INFINITY && b != -INFINITY;
         key[i] = open && !bad ? order_key(a.bias ? c[i] : l[i]) : 0u;
@@ -232,10 +257,11 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_experts_kernel(Router
         return;
     }
     if (a.bias) bmax = warp_max(bmax);
-    // a difference below this may be rounding: expf and the division are within 2^-21 of s
-    // (|l - m| <= 88 adds at most 88 2^-24 relative where s is below 2^-20 of its largest),
-    // the sum with b within 2^-24 of it
-    const float eps = 0x1p-18f;
+    // Rounding of a score s, relative: the hardware exponential is within 2^-22 plus that of
+    // its argument (d = |l|, or m - l: 2 d 2^-24), the reciprocal and products add 2^-22, a
+    // softmax's sum EPL + 5 roundings; the sum with b is within 2^-24 of c.  s <= |c| + |b|.
+    // Two sums closer than both of their bounds may be out of order.
+    const float eps0 = 0x1p-20f + (float)(EPL + 5) * 0x1p-23f;
     bool close = false;
     if (a.G > 1) {
         float mine = kNoScore;   // score of group `lane`
@@ -281,18 +307,18 @@ uint32_t b1 = 0, b2 = 0;
         if (scores) {   // the last group kept and the first left out
             const float lo = -warp_max(live && rank < a.top_groups ? -mine : -INFINITY);
             const float hi = warp_max(live && rank >= a.top_groups ? mine : -INFINITY);
-            close = hi > -INFINITY && lo - hi <= eps * (fabsf(lo) + fabsf(hi) + 2.f * bmax);
+            // (d up to 104: what is further is below 2^-149)
+            close = hi > -INFINITY && lo - hi <= (eps0 + 208.f * 0x1p-24f) * (fabsf(lo) + fabsf(hi) + 4.f * bmax);
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
             const int e = 32 * i + lane;
-            if (e < E && !((kept >> (e / n)) & 1u)) key[i] = 0u;
+            if (!((kept >> (((e * a.group_mul) >> 20) & 31)) & 1u)) key[i] = 0u;   // past E: 0 already
         }
     }
     // K rounds (one more with a bias, to see how close the first one left out is)
-    int chosen = -1;
-    uint32_t prev = 0;
-    float prev_l = 0.f, prev_b = 0.f;
+    int chosen = -1;     // lane j: the j-th
+    uint32_t ckey = 0;   // lane j: its key
     uint32_t best = 0;
     int bi = 0;
 #pragma unroll
@@ -306,28 +332,35 @@ uint32_t b1 = 0, b2 = 0;
         const uint32_t top = __reduce_max_sync(0xffffffffu, best);
         if (top == 0) break;   // uniform: nothing left
         const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(32 * bi + lane) : 0xffffffffu);
-        if (a.bias) {
-            const float el = to_f32(row[e]), eb = a.bias[e];
-            if (j > 0) {
-                const float hi = key_value(prev), lo = key_value(top);
-                close = close || (hi - lo <= eps * (fabsf(hi) + fabsf(lo) + 2.f * bmax) && !(el == prev_l && eb == prev_b));
-            }
-            prev = top;
-            prev_l = el;
-            prev_b = eb;
+        if (lane == j) {
+            chosen = e;
+            ckey = top;
         }
-        if (j < a.K && lane == j) chosen = e;
         if ((e & 31) == lane) {   // the winner's lane takes its next best
             best = 0;
+            const int wi = e >> 5;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
-                if (i == (e >> 5)) key[i] = 0u;
+                if (i == wi) key[i] = 0u;
                 if (key[i] > best) {
                     best = key[i];
                     bi = i;
                 }
             }
         }
+    }
+    if (a.bias) {   // neighbours in the order, lane j against lane j + 1
+        const float el = chosen >= 0 ? to_f32(row[chosen]) : 0.f, eb = chosen >= 0 ? a.bias[chosen] : 0.f;
+        const float v = key_value(ckey), vn = __shfl_down_sync(0xffffffffu, v, 1);
+        const float ln = __shfl_down_sync(0xffffffffu, el, 1), bn = __shfl_down_sync(0xffffffffu, eb, 1);
+        const int cn = __shfl_down_sync(0xffffffffu, chosen, 1);
+        if (lane < a.K && chosen >= 0 && cn >= 0) {
+            const float d = fminf(a.sigmoid ? fmaxf(fabsf(el), fabsf(ln)) : m - fminf(el, ln), 104.f);
+            const float tol = (eps0 + d * 0x1p-23f) * (fabsf(v) + fabsf(vn) + fabsf(eb) + fabsf(bn));
+            close = close || (v - vn <= tol && !(el == ln && eb == bn));   // equal inputs: a sure tie
+        }
+        close = __any_sync(0xffffffffu, close);
+        if (lane == a.K) chosen = -1;   // the one left out
     }
     if (close) chosen = route_row_f64<TL>(a, row, router_c64 + (size_t)warp * E);   // `close` is uniform
     // weights: lane j holds slot j
@@ -343,6 +376,13 @@ uint32_t b1 = 0, b2 = 0;
         const float tot = warp_sum(w);
         w = tot > 0.f ? w / tot : 0.f;
     } else {
+        float denom = 1.f;
+        if (!a.sigmoid) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < EPL; ++i) s += l[i] == -INFINITY ? 0.f : expf(l[i] - m);
+            denom = warp_sum(s);
+        }
         w = !on ? 0.f : (a.sigmoid ? sigmoid_f32(lj) : expf(lj - m) / denom);
     }
     if (lane < a.K) {

@@ -1,7 +1,9 @@
 """GPU parity of the 4-bit base weights against the float64 oracle: quantisation (codes,
 scales and zero points equal), its inverse, and the products.  Product bounds: a sum of n
-fp32 products in any order is within n 2^-24 of the sum of absolute values; the output is
-rounded once to bf16 (2^-8 relative)."""
+fp32 products in any order is within n 2^-24 of the sum of absolute values, and a group may
+be formed as s (sum (128 + q) x - (128 + z) sum x), whose terms' absolute values are
+s (256 + q + z) |x|; the output is rounded once to bf16 (2^-8 relative).  The norm of the
+error over a whole output is held to the rounding alone."""
 import numpy as np
 import pytest
 import torch
@@ -79,7 +81,10 @@ def reference(x, w4, bias=None):
     M = OR.w4_matrix(w4.q.cpu().numpy(), w4.scales.double().cpu().numpy(),
                      None if w4.zeros is None else w4.zeros.cpu().numpy(), w4.group)
     xn = x.double().cpu().numpy()
-    y, mag = xn @ M.T, np.abs(xn) @ np.abs(M).T
+    c, sc = OR.w4_unpack(w4.q.cpu().numpy()).astype(np.float64), w4.scales.double().cpu().numpy()
+    at = np.arange(c.shape[1]) // w4.group
+    z = 8.0 if w4.zeros is None else (w4.zeros.cpu().numpy() & 15).astype(np.float64)[:, at]
+    y, mag = xn @ M.T, np.abs(xn) @ ((256 + c + z) * np.abs(sc)[:, at]).T
     if bias is not None:
         y, mag = y + bias.double().cpu().numpy(), mag + np.abs(bias.double().cpu().numpy())
     return y, mag
