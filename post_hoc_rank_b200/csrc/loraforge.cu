@@ -1156,6 +1156,50 @@ static lf_status launch_w4_gemv(W4Args& a, const W4Maps& maps, cudaStream_t s) {
     return launch_status();
 }
 
+// Tensor map of x (T rows of d_in bf16, row stride ld): box of 64 columns x `rows` rows.
+static bool encode_x_map(CUtensorMap* map, const void* x, int32_t T, int32_t d_in, int64_t ld, int rows) {
+    const EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d_in, (cuuint64_t)T};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N>
+static lf_status launch_w4_gemm(W4Args& a, const W4mMaps& maps, cudaStream_t s) {
+    int tiles = 0, min_blocks = INT_MAX;
+    for (int p = 0; p < a.n_proj; ++p) {
+        a.p[p].tile0 = tiles;
+        tiles += (int)cdiv(a.p[p].d_out, kW4mRows);
+        min_blocks = std::min(min_blocks, (int)cdiv(a.p[p].d_in, 256));
+    }
+    const int ntt = (int)cdiv(a.T, N);
+    // CTAs of a cluster share d_in as long as all of them fit at once, each with two blocks or more
+    int cs = 1;
+    while (cs < 8 && (int64_t)tiles * ntt * cs * 2 <= 148 && min_blocks >= 4 * cs) cs *= 2;
+    constexpr size_t sm = sizeof(W4mSmem<N>);
+    LF_CUDA_TRY(cudaFuncSetAttribute(w4_gemm_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(tiles * ntt * cs));
+    cfg.blockDim = dim3(kW4mThreads);
+    cfg.dynamicSmemBytes = sm;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cs;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    PhaseScope ps("w4_gemm", s);
+    LF_CUDA_TRY(cudaLaunchKernelEx(&cfg, w4_gemm_kernel<N>, a, maps, ntt));
+    return LF_OK;
+}
+
 }  // namespace lf
 
 
@@ -2330,7 +2374,9 @@ lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_
     int order[LF_MAX_PROJECTIONS];
     for (int p = 0; p < n_proj; ++p) order[p] = p;
     std::stable_sort(order, order + n_proj, [&](int u, int v) { return projs[u].d_in > projs[v].d_in; });
-    W4Maps maps;
+    const bool many = T > 16;   // tcgen05 tiles of N tokens; few: the streaming kernel, 8 or 16 at a time
+    const int N = T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    W4mMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     bool wide = true;   // every group holds whole 128-column pieces
     for (int i = 0; i < n_proj; ++i) {
@@ -2338,7 +2384,8 @@ lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_
         W4Proj& t = a.p[i];
         t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
         t.y = reinterpret_cast<__nv_bfloat16*>(q.y);
-        if (!encode_q_map(&maps.q[i], q.q, q.d_out, q.d_in, kW4Rows)) return LF_ERR_CUDA;
+        if (!encode_q_map(&maps.q[i], q.q, q.d_out, q.d_in, many ? kW4mRows : kW4Rows)) return LF_ERR_CUDA;
+        if (many && !encode_x_map(&maps.x[i], q.x, T, q.d_in, q.x_ld, N)) return LF_ERR_CUDA;
         wide = wide && q.group >= 128;
         t.scales = reinterpret_cast<const __nv_bfloat16*>(q.scales);
         t.zeros = reinterpret_cast<const uint8_t*>(q.zeros);
@@ -2353,8 +2400,11 @@ lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_
     (void)ws;
     (void)ws_bytes;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (T <= 8) return wide ? launch_w4_gemv<1, true>(a, maps, s) : launch_w4_gemv<1, false>(a, maps, s);
-    return wide ? launch_w4_gemv<2, true>(a, maps, s) : launch_w4_gemv<2, false>(a, maps, s);
+    if (many) return N == 32 ? launch_w4_gemm<32>(a, maps, s) : N == 64 ? launch_w4_gemm<64>(a, maps, s) : launch_w4_gemm<128>(a, maps, s);
+    W4Maps qmaps;
+    std::memcpy(qmaps.q, maps.q, sizeof(qmaps.q));
+    if (T <= 8) return wide ? launch_w4_gemv<1, true>(a, qmaps, s) : launch_w4_gemv<1, false>(a, qmaps, s);
+    return wide ? launch_w4_gemv<2, true>(a, qmaps, s) : launch_w4_gemv<2, false>(a, qmaps, s);
 }
 
 lf_status lf_check_bounded_wait(int32_t polls, lf_stream_t stream) {

@@ -8,6 +8,7 @@
 // ng = ceil(d_in / group) (the last group may be short).  A weight is (q - z) * s.
 #pragma once
 #include <cuda.h>   // CUtensorMap (type only)
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include "apply_common.cuh"
@@ -476,6 +477,286 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_gemv_kernel(const __grid_
         if (P.bias) v += __bfloat162float(P.bias[row0 + r]);
         P.y[(int64_t)(tok0 + n) * P.y_ld + row0 + r] = __float2bfloat16_rn(v);
     }
+}
+
+// ---- product, many tokens ------------------------------------------------------------------
+// CTA (128 rows of one projection, N tokens, a share of d_in): D = W x^T on tcgen05 with the
+// weights as the 128-row operand A.  A comes from tensor memory: a thread unpacks its row's
+// codes (lane = row there) and stores q - z as bf16 pairs, so the unpacked weights never
+// touch shared memory, whose bandwidth would bound the product (128 columns of 128 rows:
+// 32 KB written and 32 KB read against 512 cycles of products at N = 128).  Blocks of 256
+// columns: one code stage, four x boxes, one A buffer.
+//   warps 0-7, unpack: two warpgroups take the blocks in turn; codes by TMA (boxes of 128 rows
+//     x 128 bytes), exact q - z, tcgen05.st (11 integer instructions per 8 weights, 704 cycles
+//     of an SM per block: about the rate at which HBM delivers the codes);
+//   warps 8-15, sums: each group's product leaves tensor memory and is added to fp32 registers
+//     times the row's scale (A stays exact, and a group's scale multiplies once, in fp32);
+//     two product buffers, so that the next group runs meanwhile;
+//   warps 16, 17: TMA of the codes, of x;  warp 18: issues the products, converged, so that
+//     the descriptors stay in uniform registers (issued from a branch of one lane, each
+//     product took 100 to 270 cycles of that lane's own instructions).
+// CS CTAs of a cluster share d_in when there are few tiles; they add up over distributed
+// shared memory in rank order.
+constexpr int kW4mThreads = 19 * 32;
+constexpr int kW4mRows = 128;
+constexpr int kW4mX = 2;      // x stages: N tokens x 256 columns
+// code stages (128 rows x 256 columns, 16 KB): with few tokens the reads of the codes bound
+// the kernel, and what x leaves of shared memory keeps them in flight
+constexpr int w4m_q(int N) { return N == 128 ? 5 : 8; }
+
+struct alignas(64) W4mMaps {
+    CUtensorMap q[kW4MaxProj];   // box 128 bytes x 128 rows, 128-byte swizzle
+    CUtensorMap x[kW4MaxProj];   // box 64 columns x N rows, 128-byte swizzle
+};
+
+template <int N>
+struct W4mSmem {
+    static constexpr int kW4mQ = w4m_q(N);
+    union {
+        struct {
+            unsigned char q[kW4mQ][kW4mRows * 128];
+            unsigned char x[kW4mX][4][N * 128];       // four pieces of 64 columns
+        };
+        float part[N][kW4mRows];                      // this CTA's sums, for the cluster
+    };
+    uint64_t qfull[kW4mQ], qempty[kW4mQ], xfull[kW4mX], xempty[kW4mX], afull[2], aempty[2], dfull[2], dempty[2];
+    uint32_t tmem;
+    int32_t failed;
+};
+
+// 8 columns (one word) as four bf16 pairs of q - z in column order
+__device__ __forceinline__ void unpack_word(uint32_t w, __nv_bfloat162 z, uint32_t* out) {
+    const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t p = __byte_perm(even, odd, (uint32_t)(i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12)));
+        p = (p & 0x00FF00FFu) | 0x43004300u;   // 128 + q
+        const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&p), z);
+        out[i] = *reinterpret_cast<const uint32_t*>(&d);
+    }
+}
+
+constexpr uint32_t kW4mAcol = 256;   // two product buffers of N <= 128 columns, then two A buffers of 128
+
+// The products of a CTA's nb blocks, 2^LOGD groups in each: one converged warp.
+template <int N, int LOGD>
+__device__ __forceinline__ bool w4m_products(W4mSmem<N>& s, uint32_t tmem_any, int nb) {
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_any, 0);
+    const uint32_t idesc = tc::idesc_bf16(kW4mRows, N, 0, 0);
+    const uint64_t xdesc = tc::smem_desc_sw128(s.x[0][0]);
+    constexpr int per = 16 >> LOGD;   // K = 16 steps of a group's piece
+    int d = 0;
+    for (int b = 0; b < nb; ++b) {
+        const uint64_t xd = xdesc + (uint64_t)((b % kW4mX) * (4 * N * 128 / 16));
+        const uint32_t ad = tmem + kW4mAcol + 128 * (b & 1);
+        bool ok = mbar_wait(&s.xfull[b % kW4mX], (uint32_t)(b / kW4mX) & 1) && mbar_wait(&s.afull[b & 1], (uint32_t)(b >> 1) & 1);
+#pragma unroll
+        for (int g = 0; g < (1 << LOGD); ++g, ++d) {
+            if (d >= 2) ok = ok && mbar_wait(&s.dempty[d & 1], (uint32_t)((d >> 1) - 1) & 1);
+            if (!__all_sync(0xffffffffu, ok)) return false;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int i = 0; i < per; ++i) {
+                const int k = g * per + i;
+                tc::mma_bf16_ta_warp(tmem + (uint32_t)((d & 1) * N), ad + 8 * k,
+                                     xd + (uint64_t)((k >> 2) * (N * 128 / 16) + 2 * (k & 3)), idesc, i > 0);
+            }
+            tc::commit_warp(&s.dfull[d & 1]);
+        }
+        tc::commit_warp(&s.xempty[b % kW4mX]);
+        tc::commit_warp(&s.aempty[b & 1]);
+    }
+    // every product has completed before the buffers are reused or the CTA leaves
+    bool ok = nb == 0 || mbar_wait(&s.aempty[(nb - 1) & 1], (uint32_t)((nb - 1) >> 1) & 1);
+    return __all_sync(0xffffffffu, ok);
+}
+
+template <int N>
+__global__ void __launch_bounds__(kW4mThreads, 1) w4_gemm_kernel(const __grid_constant__ W4Args a,
+                                                                 const __grid_constant__ W4mMaps maps, int n_tok_tiles) {
+    namespace cg = cooperative_groups;
+    constexpr uint32_t kTmemCols = 512;
+    constexpr int NH = N / 2;              // tokens per sum thread
+    constexpr int kW4mQ = w4m_q(N);
+    extern __shared__ __align__(1024) unsigned char w4_raw[];
+    auto& s = *reinterpret_cast<W4mSmem<N>*>(w4_raw);
+    cg::cluster_group cl = cg::this_cluster();
+    const int CS = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    const int tile = (int)blockIdx.x / CS / n_tok_tiles;
+    const int tok0 = ((int)blockIdx.x / CS % n_tok_tiles) * N;
+    int pi = 0;
+#pragma unroll
+    for (int i = 1; i < kW4MaxProj; ++i)
+        if (i < a.n_proj && tile >= a.p[i].tile0) pi = i;
+    const W4Proj& P = a.p[pi];
+    const int row0 = (tile - P.tile0) * kW4mRows;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int blocks = (P.d_in + 255) >> 8;
+    const int b0 = (int)((int64_t)blocks * rank / CS);                        // this CTA's blocks: b0 ..
+    const int nb = (int)((int64_t)blocks * (rank + 1) / CS) - b0;
+    const int log_u = P.log_u, log_d = 3 - log_u;                             // log2 of groups per block
+    if (warp == 0) tc::tmem_alloc(&s.tmem, kTmemCols);
+    if (tid == 0) {
+        for (int i = 0; i < kW4mQ; ++i) {
+            mbar_init(&s.qfull[i], 1);
+            mbar_init(&s.qempty[i], 4);
+        }
+        for (int i = 0; i < kW4mX; ++i) {
+            mbar_init(&s.xfull[i], 1);
+            mbar_init(&s.xempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.afull[i], 4);
+            mbar_init(&s.aempty[i], 1);
+            mbar_init(&s.dfull[i], 1);
+            mbar_init(&s.dempty[i], 8);
+        }
+        s.failed = 0;
+        fence_barrier_init();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s.tmem;
+    const int row = row0 + 32 * (warp & 3) + lane;                 // unpack and sum threads
+    const int64_t grow = (int64_t)min(row, P.d_out - 1) * P.ng;    // rows past the last: any
+    bool ok = true;
+    if (warp < 8) {   // ---- unpack: blocks b = warpgroup, warpgroup + 2, ..
+        const int r = 32 * (warp & 3) + lane, wg = warp >> 2;
+        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kW4mAcol + 128 * wg;
+        const uint8_t* zrow = P.zeros ? P.zeros + grow : nullptr;
+        for (int b = wg; b < nb && ok; b += 2) {
+            const int qs = b % kW4mQ;
+            uint32_t z[8];   // 0x4300 + zero point of each 32-column unit (a group covers 1, 2, 4 or 8)
+            if (zrow) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    z[u] = (u & ((1 << log_u) - 1)) == 0 ? zrow[min(((b0 + b) * 8 + u) >> log_u, P.ng - 1)] : z[u > 0 ? u - 1 : 0];
+            } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) z[u] = 8u;
+            }
+            ok = mbar_wait(&s.qfull[qs], (uint32_t)(b / kW4mQ) & 1);
+            if (b >= 2) ok = ok && mbar_wait(&s.aempty[wg], (uint32_t)((b >> 1) - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            tc::fence_after_sync();   // the products that read this buffer are complete (aempty)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {   // 64 columns: 32 columns of tensor memory
+                uint32_t o[32];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int c = 2 * q + h;   // 16-byte piece of the row
+                    const uint4 w = *reinterpret_cast<const uint4*>(s.q[qs] + r * 128 + ((c ^ (r & 7)) << 4));
+                    const uint32_t zz = (0x4300u + (z[c] & 15u)) * 0x10001u;
+                    const __nv_bfloat162 zp = *reinterpret_cast<const __nv_bfloat162*>(&zz);
+                    unpack_word(w.x, zp, o + 16 * h);
+                    unpack_word(w.y, zp, o + 16 * h + 4);
+                    unpack_word(w.z, zp, o + 16 * h + 8);
+                    unpack_word(w.w, zp, o + 16 * h + 12);
+                }
+                tc::tmem_st32(at + 32 * q, o);
+            }
+            tc::tmem_wait_st();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive1(&s.afull[wg]);
+                mbar_arrive1(&s.qempty[qs]);
+            }
+        }
+    } else if (warp < 16) {   // ---- sums: NH of the tokens, every group's product
+        const int half = (warp - 8) >> 2;
+        const int nd = nb << log_d;
+        const __nv_bfloat16* srow = P.scales + grow;
+        const int g0 = b0 << log_d;
+        const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(half * NH);
+        float acc[NH];
+#pragma unroll
+        for (int i = 0; i < NH; ++i) acc[i] = 0.f;
+        float next = nd > 0 ? __bfloat162float(srow[min(g0, P.ng - 1)]) : 0.f;
+        for (int d = 0; d < nd && ok; ++d) {
+            const float sc = next;
+            next = __bfloat162float(srow[min(g0 + d + 1, P.ng - 1)]);   // arrives while this one is waited for
+            ok = __all_sync(0xffffffffu, mbar_wait(&s.dfull[d & 1], (uint32_t)(d >> 1) & 1));
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < NH / 16; ++c) {
+                float v[16];
+                tc::tmem_ld16(at + (uint32_t)((d & 1) * N + 16 * c), v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[16 * c + i] = fmaf(sc, v[i], acc[16 * c + i]);
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(&s.dempty[d & 1]);
+        }
+        if (ok && CS == 1) {
+            const int t0 = tok0 + half * NH;
+            const float bias = P.bias ? __bfloat162float(P.bias[min(row, P.d_out - 1)]) : 0.f;
+#pragma unroll
+            for (int i = 0; i < NH; ++i)
+                if (row < P.d_out && t0 + i < a.T)
+                    P.y[(int64_t)(t0 + i) * P.y_ld + row] = __float2bfloat16_rn(acc[i] + bias);
+        } else if (ok) {   // the last product has read the last stage: the stages become this CTA's sums
+#pragma unroll
+            for (int i = 0; i < NH; ++i) s.part[half * NH + i][32 * (warp & 3) + lane] = acc[i];
+        }
+    } else if (warp == 16) {   // ---- TMA of the codes
+        if (lane == 0) {
+            int i = 0;   // stages issued
+            for (; i < nb; ++i) {
+                const int st = i % kW4mQ;
+                if (i >= kW4mQ) ok = mbar_wait(&s.qempty[st], (uint32_t)(i / kW4mQ - 1) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&s.qfull[st], kW4mRows * 128);
+                tc::tma_load_2d(s.q[st], &maps.q[pi], (b0 + i) * 128, row0, &s.qfull[st]);
+            }
+            // nothing is in flight when the buffers are reused or the CTA leaves
+            for (int j = max(0, i - kW4mQ); j < i; ++j) ok = mbar_wait(&s.qfull[j % kW4mQ], (uint32_t)(j / kW4mQ) & 1) && ok;
+        }
+    } else if (warp == 17) {   // ---- TMA of x
+        if (lane == 0) {
+            int i = 0;
+            for (; i < nb; ++i) {
+                const int st = i % kW4mX;
+                if (i >= kW4mX) ok = mbar_wait(&s.xempty[st], (uint32_t)(i / kW4mX - 1) & 1);
+                if (!ok) break;
+                mbar_arrive_expect_tx(&s.xfull[st], 4 * N * 128);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    tc::tma_load_2d(s.x[st][q], &maps.x[pi], (b0 + i) * 256 + 64 * q, tok0, &s.xfull[st]);
+            }
+            for (int j = max(0, i - kW4mX); j < i; ++j) ok = mbar_wait(&s.xfull[j % kW4mX], (uint32_t)(j / kW4mX) & 1) && ok;
+        }
+    } else {   // ---- products
+        ok = log_d == 0   ? w4m_products<N, 0>(s, tmem, nb)
+             : log_d == 1 ? w4m_products<N, 1>(s, tmem, nb)
+             : log_d == 2 ? w4m_products<N, 2>(s, tmem, nb)
+                          : w4m_products<N, 3>(s, tmem, nb);
+    }
+    if (!ok) s.failed = 1;
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
+    if (CS == 1) return;
+    cl.sync();
+    bool all_ok = true;
+    for (int c = 0; c < CS; ++c) all_ok = all_ok && *cl.map_shared_rank(&s.failed, c) == 0;
+    // this CTA's share of the tokens, summed over the cluster in rank order
+    const int nt = min(N, a.T - tok0);
+    const int n0 = nt * rank / CS, n1 = all_ok ? nt * (rank + 1) / CS : n0;   // a timeout is latched
+    for (int o = tid; o < (n1 - n0) * kW4mRows; o += kW4mThreads) {
+        const int n = n0 + o / kW4mRows, r = o % kW4mRows;
+        if (row0 + r >= P.d_out) continue;
+        float v = 0.f;
+        for (int c = 0; c < CS; ++c) v += cl.map_shared_rank(&s.part[n][r], c)[0];
+        if (P.bias) v += __bfloat162float(P.bias[row0 + r]);
+        P.y[(int64_t)(tok0 + n) * P.y_ld + row0 + r] = __float2bfloat16_rn(v);
+    }
+    cl.sync();   // the parts are read by the whole cluster
 }
 
 }  // namespace lf
