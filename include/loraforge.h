@@ -507,10 +507,14 @@ lf_status lf_route_experts_backward(int32_t T, const lf_router* router /*[host]*
  *          dx_base NULL = zeros, may be dx itself)
  *   grad_weights[t][j] = sum over the call's projections of s_j <B'^T dy_t, A'_{e_tj} x_t>
  *          (fp32, projections in order; slots of -1 get 0; NULL = not wanted).
- * Workspace for either: lf_lora_mixture_workspace_size(T, top_k, n_adapters, n_proj,
- * max_rank), max_rank = the largest max_rank of the projections (0 where one is 0);
- * 0 bytes when none is needed (ws may then be NULL).  Results are the same from run to
- * run; a batch size may change the order of sums. */
+ * A long batch over a small pool (few stacked rows, n_adapters * max_rank; max_rank 0 counts
+ * as 64) runs on the tensor cores as two dense products over the whole pool, with the
+ * intermediates carried as two bf16 values (16 significant bits); other batches token by
+ * token.  On the dense path an adapter's factors that are not finite give NaN in the whole
+ * slice of the tokens that use it (and in no other).
+ * Workspace: lf_lora_mixture_workspace_size / lf_lora_mixture_backward_workspace_size bytes
+ * for the same arguments (0: ws may be NULL).  Results are the same from run to run; a batch
+ * size may change the order of sums. */
 typedef struct {
     const void* x;              /* T rows of x_ld bf16 */
     const void* base;           /* nullable: T rows of y_ld bf16 */
@@ -530,7 +534,10 @@ typedef struct {
     int64_t x_ld, dy_ld, dx_ld;
     lf_slice slice;             /* y_offset: first column of the slice in dy */
 } lf_mixture_grad;
-size_t lf_lora_mixture_workspace_size(int32_t T, int32_t top_k, int32_t n_adapters, int32_t n_proj, int32_t max_rank);
+size_t lf_lora_mixture_workspace_size(int32_t T, int32_t top_k, int32_t n_adapters,
+                                      const lf_mixture_projection* projs /*[host]*/, int32_t n_proj);
+size_t lf_lora_mixture_backward_workspace_size(int32_t T, int32_t top_k, int32_t n_adapters,
+                                               const lf_mixture_grad* projs /*[host]*/, int32_t n_proj);
 lf_status lf_lora_mixture(int32_t T, int32_t top_k, const int32_t* ids, const float* weights, int32_t n_adapters,
                           const lf_mixture_projection* projs /*[host]*/, int32_t n_proj, float scale,
                           const float* adapter_scale, void* ws, size_t ws_bytes, lf_stream_t stream);

@@ -270,13 +270,6 @@ def _same_rows(projections, T: int):
         raise ValueError(f"every projection must have {T} rows, got {[p.rows for p in projections]}")
 
 
-def _mixture_ws(ids, n_adapters: int, projections):
-    ranks = [p.slice.max_rank for p in projections]
-    n = lf.lf_lora_mixture_workspace_size(ids.shape[0], ids.shape[1], n_adapters, len(projections),
-                                          0 if 0 in ranks else max(ranks))
-    return workspace(n, ids.device) if n else None
-
-
 def lora_mixture(ids, weights, n_adapters: int, projections, scale: float, adapter_scale=None, ws=None, stream=None):
     """Routed side path (lf_lora_mixture) of lf.make_mixture_projection projections, whose y it
     writes: y = base + scale * sum_j weights_j B'_j (A'_j x).  ids T x top_k int32 (-1 = empty
@@ -287,7 +280,9 @@ def lora_mixture(ids, weights, n_adapters: int, projections, scale: float, adapt
     _expect(adapter_scale, "adapter_scale", dev, torch.float32, (n_adapters,))
     _same_rows(projections, ids.shape[0])
     with _on(dev):
-        ws = ws if ws is not None else _mixture_ws(ids, n_adapters, projections)
+        if ws is None:
+            n = lf.lf_lora_mixture_workspace_size(ids.shape[0], ids.shape[1], n_adapters, projections)
+            ws = workspace(n, dev) if n else None
         lf.lf_lora_mixture(ids, weights, n_adapters, projections, scale, ws, adapter_scale, stream)
 
 
@@ -303,7 +298,9 @@ def lora_mixture_backward(ids, weights, n_adapters: int, grads, scale: float, ad
     _same_rows(grads, ids.shape[0])
     with _on(dev):
         gw = torch.empty(ids.shape, dtype=torch.float32, device=dev) if grad_weights else None
-        ws = ws if ws is not None else _mixture_ws(ids, n_adapters, grads)
+        if ws is None:
+            n = lf.lf_lora_mixture_backward_workspace_size(ids.shape[0], ids.shape[1], n_adapters, grads)
+            ws = workspace(n, dev) if n else None
         lf.lf_lora_mixture_backward(ids, weights, n_adapters, grads, scale, gw, ws, adapter_scale, stream)
     return gw
 

@@ -20,6 +20,7 @@
 #include "pool.cuh"
 #include "router.cuh"
 #include "mixture.cuh"
+#include "mixture_tc.cuh"
 #include "w4.cuh"
 
 namespace lf {
@@ -1093,8 +1094,217 @@ static void mix_tables(MixProj& t, const lf_slice& q, int32_t d_in) {
     t.pool_Bt = q.pool_elems_Bt;
 }
 
-static size_t mix_ws_bytes(int64_t T, int K, int n_proj) {   // per-projection weight gradients
-    return n_proj > 1 ? (size_t)T * K * n_proj * sizeof(float) + 256 : 0;
+// Tensor map of T rows of d_in bf16 (row stride ld): box of 64 columns x `rows` rows, 128-byte
+// swizzle; what lies outside reads as zeros and is not written.
+static bool encode_x_map(CUtensorMap* map, const void* x, int32_t T, int32_t d_in, int64_t ld, int rows) {
+    const EncodeTiledFn fn = encode_tiled_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d_in, (cuuint64_t)T};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)rows};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether a projection goes over the whole pool on the tensor cores: a pool of at most kMtRows
+// stacked rows (by the bound the caller gives), and a batch long enough.  Costs in us,
+// measured on 3584 x 3584 and 3584 x 18944: token by token, the factor rows of every slot from
+// L2 at about 5 TB/s (half the rank bound on average); dense, four launches and the packed
+// copy, then 6 operations per (token, stacked row, column) at about 600 TFLOP/s.
+static bool mix_dense(int64_t T, int K, int64_t n_adapters, int max_rank, int64_t d_in, int64_t d_out) {
+    const int64_t rmax = n_adapters * (max_rank > 0 ? max_rank : kMaxRank);
+    if (rmax > kMtRows) return false;
+    const double d = (double)(d_in + d_out), rank = 0.5 * (double)(max_rank > 0 ? max_rank : kMaxRank);
+    const double token = (double)T * K * rank * d * 2.0 / 5e6;
+    const double dense = 20.0 + (double)rmax * d * 4.0 / 3e6 + (double)T * (double)rmax * d * 6.0 / 6e8;
+    return dense < token;
+}
+static int mix_rows(int64_t n_adapters, int max_rank) {   // rows of the packed matrices
+    return (int)align_up(n_adapters * (max_rank > 0 ? max_rank : kMaxRank), kMtKB);
+}
+
+struct MixTcWs {
+    MixPlan* plan;
+    __nv_bfloat16 *A, *Bt, *hi, *lo;
+    float *S, *U, *gw;
+};
+// Carves (base == nullptr: sizes) the dense path's workspace for one projection.
+static size_t carve_mix(void* base, int64_t T, int64_t Rp, int64_t d_in, int64_t d_out, bool grad, MixTcWs* w) {
+    Carver c(base);
+    w->plan = c.take<MixPlan>(1);
+    w->A = c.take<__nv_bfloat16>((size_t)(Rp * d_in));
+    w->Bt = c.take<__nv_bfloat16>((size_t)(Rp * d_out));
+    w->hi = c.take<__nv_bfloat16>((size_t)(T * Rp));
+    w->lo = c.take<__nv_bfloat16>((size_t)(T * Rp));
+    w->S = c.take<float>(grad ? (size_t)(T * Rp) : 0);
+    w->U = c.take<float>(grad ? (size_t)(T * Rp) : 0);
+    return c.off + 512;
+}
+
+// Host checks of a call's projections, then the kernel tables.
+static lf_status mix_projection(const lf_mixture_projection& q, MixProj& t) {
+    if (q.reserved != 0) return LF_ERR_INVALID_ARG;
+    const lf_status cs = check_apply(q.d_in, q.x, q.y, q.y_ld, &q.slice, 1, false);
+    if (cs != LF_OK) return cs;
+    if (q.x_ld < q.d_in) return LF_ERR_INVALID_ARG;
+    if ((q.x_ld & 7) || !aligned16(q.base)) return LF_ERR_ALIGNMENT;
+    mix_tables(t, q.slice, q.d_in);
+    t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
+    t.in2 = reinterpret_cast<const __nv_bfloat16*>(q.base);
+    t.base = nullptr;
+    t.out = reinterpret_cast<__nv_bfloat16*>(q.y);
+    t.x_ld = q.x_ld;
+    t.out_ld = q.y_ld;
+    return LF_OK;
+}
+static lf_status mix_projection(const lf_mixture_grad& q, MixProj& t) {
+    if (q.reserved != 0) return LF_ERR_INVALID_ARG;
+    const lf_status cs = check_apply(q.d_in, q.x, q.dy, q.dy_ld, &q.slice, 1, false);
+    if (cs != LF_OK) return cs;
+    if (q.x_ld < q.d_in || (q.dx && q.dx_ld < q.d_in) || (q.dx_base && !q.dx)) return LF_ERR_INVALID_ARG;
+    if ((q.x_ld & 7) || (q.dx && (q.dx_ld & 7)) || !aligned16(q.dx) || !aligned16(q.dx_base)) return LF_ERR_ALIGNMENT;
+    mix_tables(t, q.slice, q.d_in);
+    t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
+    t.in2 = reinterpret_cast<const __nv_bfloat16*>(q.dy);
+    t.base = reinterpret_cast<const __nv_bfloat16*>(q.dx_base);
+    t.out = reinterpret_cast<__nv_bfloat16*>(q.dx);
+    t.x_ld = q.x_ld;
+    t.dy_ld = q.dy_ld;
+    t.out_ld = q.dx_ld;
+    return LF_OK;
+}
+
+static bool mix_proj_dense(int64_t T, int K, int64_t n, const lf_slice& s, int32_t d_in) {
+    return mix_dense(T, K, n, s.max_rank, d_in, s.d_out);
+}
+template <typename P>
+static size_t mix_ws_size(int32_t T, int32_t K, int32_t n_adapters, const P* projs, int32_t n_proj, bool grad) {
+    if (T < 0 || K < 1 || K > kMixMaxK || n_adapters < 1 || n_adapters > 16384 || n_proj < 1 || n_proj > kMaxProj || !projs)
+        return 0;
+    size_t most = 0;
+    MixTcWs w;
+    for (int p = 0; p < n_proj; ++p)
+        if (mix_proj_dense(T, K, n_adapters, projs[p].slice, projs[p].d_in))
+            most = std::max(most, carve_mix(nullptr, T, mix_rows(n_adapters, projs[p].slice.max_rank), projs[p].d_in,
+                                            projs[p].slice.d_out, grad, &w));
+    if (grad && n_proj > 1) most += (size_t)T * K * n_proj * sizeof(float) + 512;   // per-projection weight gradients
+    return most;
+}
+
+static lf_status launch_mix_shrink(const MixShrinkArgs& a, int Rmax, const CUtensorMap& xmap, const CUtensorMap& amap,
+                                   cudaStream_t s) {
+    const int tiles = (int)cdiv(a.T, kMtM), chunks = (int)cdiv(Rmax, kMtN), steps = (int)cdiv(a.d, kMtKB);
+    int cs = 1;   // shares of d: as many CTAs as SMs, four stages or more each
+    while (cs < 8 && 2 * cs * tiles * chunks <= 148 && steps >= 8 * cs) cs *= 2;
+    constexpr size_t sm = sizeof(MixShrinkSmem);
+    LF_CUDA_TRY(cudaFuncSetAttribute(mixture_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(tiles * cs), (unsigned)chunks);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = sm;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)cs;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    PhaseScope ps("mixture_shrink", s);
+    LF_CUDA_TRY(cudaLaunchKernelEx(&cfg, mixture_shrink_kernel, a, xmap, amap));
+    return LF_OK;
+}
+
+// One projection on the dense path.  grad: P is a gradient's table (in2 = dy, out = dx).
+static lf_status mix_dense_projection(const MixArgs& A, const MixProj& P, bool grad, float* gw, void* ws, cudaStream_t s) {
+    const int64_t T = A.T;
+    const int Rp = mix_rows(A.n_adapters, P.max_rank);
+    const int Rmax = A.n_adapters * (P.max_rank > 0 ? P.max_rank : kMaxRank);
+    MixTcWs w;
+    carve_mix(reinterpret_cast<char*>(align_up((int64_t)reinterpret_cast<uintptr_t>(ws), 256)), T, Rp, P.d_in, P.d_out, grad, &w);
+    alignas(64) CUtensorMap xm, dym, am, bm, ab, bb, him, lom, basem, outm;
+    bool ok = encode_x_map(&xm, P.x, A.T, P.d_in, P.x_ld, kMtM) && encode_x_map(&am, w.A, Rp, P.d_in, P.d_in, kMtN) &&
+              encode_x_map(&him, w.hi, A.T, Rp, Rp, kMtM) && encode_x_map(&lom, w.lo, A.T, Rp, Rp, kMtM);
+    if (grad) ok = ok && encode_x_map(&dym, P.in2 + P.y_off, A.T, P.d_out, P.dy_ld, kMtM) &&
+                   encode_x_map(&bm, w.Bt, Rp, P.d_out, P.d_out, kMtN);
+    const bool expand = !grad || P.out;
+    const int dout = grad ? P.d_in : P.d_out;   // columns the expand writes
+    const __nv_bfloat16* base = grad ? P.base : (P.in2 ? P.in2 + P.y_off : nullptr);
+    if (expand) {
+        __nv_bfloat16* out = grad ? P.out : P.out + P.y_off;
+        ok = ok && encode_x_map(&outm, out, A.T, dout, P.out_ld, kMtM) &&
+             encode_x_map(&basem, base ? base : out, A.T, dout, P.out_ld, kMtM) &&
+             encode_x_map(grad ? &ab : &bb, grad ? w.A : w.Bt, Rp, dout, dout, kMtKB);
+    }
+    if (!ok) return LF_ERR_CUDA;
+    MixPackArgs pa{A.n_adapters, P.max_rank, P.d_in, P.d_out, Rp, P.ranks, P.off_A, P.off_Bt, P.A_pool, P.Bt_pool,
+                   P.pool_A, P.pool_Bt, w.plan, w.A, w.Bt};
+    LF_LAUNCH("mixture_pack", mixture_pack_kernel, dim3((unsigned)Rp, 2), 256, 0, s, pa);
+    LF_CUDA_TRY(cudaGetLastError());
+    MixShrinkArgs sh{A.T, A.K, A.n_adapters, P.d_in, Rp, 1, w.plan, A.ids, A.weights, A.scale, A.scales, nullptr, nullptr, nullptr};
+    if (!grad) {
+        sh.hi = w.hi;
+        sh.lo = w.lo;
+        const lf_status st = launch_mix_shrink(sh, Rmax, xm, am, s);
+        if (st != LF_OK) return st;
+    } else {
+        if (gw) {   // S = A x
+            sh.raw = w.S;
+            const lf_status st = launch_mix_shrink(sh, Rmax, xm, am, s);
+            if (st != LF_OK) return st;
+            sh.raw = w.U;
+            sh.report = 0;
+        }
+        sh.d = P.d_out;   // U = B^T dy
+        if (P.out) {
+            sh.hi = w.hi;
+            sh.lo = w.lo;
+        }
+        const lf_status st = launch_mix_shrink(sh, Rmax, dym, bm, s);
+        if (st != LF_OK) return st;
+        if (gw) {
+            MixDotArgs da{A.T, A.K, A.n_adapters, Rp, w.plan, A.ids, A.scale, A.scales, w.S, w.U, gw};
+            LF_LAUNCH("mixture_dot", mixture_dot_kernel, (unsigned)cdiv(T, 8), 256, 0, s, da);
+            LF_CUDA_TRY(cudaGetLastError());
+        }
+    }
+    if (!expand) return LF_OK;
+    const int tiles = (int)(cdiv(dout, kMtN) * cdiv(T, kMtM));
+    MixExpandArgs ea{A.T, dout, base ? 1 : 0, 0, w.plan};
+    constexpr size_t sm = sizeof(MixExpandSmem);
+    LF_CUDA_TRY(cudaFuncSetAttribute(mixture_expand_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+    LF_LAUNCH("mixture_expand", mixture_expand_kernel, (unsigned)std::min(tiles, 148), kMtExpandThreads, sm, s, ea, him, lom,
+              grad ? ab : bb, basem, outm);
+    return launch_status();
+}
+
+// Every projection on its path: the dense ones one after the other, the rest in one launch.
+// gw: n_proj x T x K partial sums, or the result itself for one projection (nullable).
+template <bool GRAD>
+static lf_status mix_run(MixArgs& A, float* gw, void* ws, cudaStream_t s) {
+    MixArgs B = A;   // the token-parallel projections, in order
+    B.n_proj = 0;
+    bool dense[kMaxProj];
+    for (int p = 0; p < A.n_proj; ++p) {
+        dense[p] = mix_dense(A.T, A.K, A.n_adapters, A.p[p].max_rank, A.p[p].d_in, A.p[p].d_out);
+        if (!dense[p]) B.p[B.n_proj++] = A.p[p];
+    }
+    int tok = 0;
+    for (int p = 0; p < A.n_proj; ++p) {
+        if (!dense[p]) {
+            ++tok;
+            continue;
+        }
+        // partial gradients: the token-parallel projections' first, then the dense ones'
+        float* g = gw ? gw + (int64_t)(B.n_proj + p - tok) * A.T * A.K : nullptr;
+        const lf_status st = mix_dense_projection(A, A.p[p], GRAD, g, ws, s);
+        if (st != LF_OK) return st;
+    }
+    if (B.n_proj == 0) return LF_OK;
+    B.gw = gw;
+    return launch_mixture_token<GRAD>(B, s);
 }
 
 // ------------------------------------------------------------------ 4-bit base weights
@@ -1154,19 +1364,6 @@ static lf_status launch_w4_gemv(W4Args& a, const W4Maps& maps, cudaStream_t s) {
     LF_LAUNCH("w4_gemv", (w4_gemv_kernel<NT, WIDE>), dim3((unsigned)tiles, (unsigned)cdiv(a.T, 8 * NT)), 32 * kW4Warps,
               sm, s, a, maps);
     return launch_status();
-}
-
-// Tensor map of x (T rows of d_in bf16, row stride ld): box of 64 columns x `rows` rows.
-static bool encode_x_map(CUtensorMap* map, const void* x, int32_t T, int32_t d_in, int64_t ld, int rows) {
-    const EncodeTiledFn fn = encode_tiled_fn();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)d_in, (cuuint64_t)T};
-    const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(x), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int N>
@@ -2221,11 +2418,14 @@ lf_status lf_route_experts_backward(int32_t T, const lf_router* router, const vo
     return LF_OK;
 }
 
-size_t lf_lora_mixture_workspace_size(int32_t T, int32_t top_k, int32_t n_adapters, int32_t n_proj, int32_t max_rank) {
-    if (T < 0 || top_k < 1 || top_k > kMixMaxK || n_adapters < 1 || n_adapters > 16384 || n_proj < 1 ||
-        n_proj > kMaxProj || max_rank < 0 || max_rank > kMaxRank)
-        return 0;
-    return mix_ws_bytes(T, top_k, n_proj);
+size_t lf_lora_mixture_workspace_size(int32_t T, int32_t top_k, int32_t n_adapters, const lf_mixture_projection* projs,
+                                      int32_t n_proj) {
+    return mix_ws_size(T, top_k, n_adapters, projs, n_proj, false);
+}
+
+size_t lf_lora_mixture_backward_workspace_size(int32_t T, int32_t top_k, int32_t n_adapters, const lf_mixture_grad* projs,
+                                               int32_t n_proj) {
+    return mix_ws_size(T, top_k, n_adapters, projs, n_proj, true);
 }
 
 lf_status lf_lora_mixture(int32_t T, int32_t top_k, const int32_t* ids, const float* weights, int32_t n_adapters,
@@ -2243,23 +2443,13 @@ lf_status lf_lora_mixture(int32_t T, int32_t top_k, const int32_t* ids, const fl
     A.scale = scale;
     A.scales = adapter_scale;
     for (int p = 0; p < n_proj; ++p) {
-        const lf_mixture_projection& q = projs[p];
-        if (q.reserved != 0) return LF_ERR_INVALID_ARG;
-        const lf_status cs = check_apply(q.d_in, q.x, q.y, q.y_ld, &q.slice, 1, false);
-        if (cs != LF_OK) return cs;
-        if (q.x_ld < q.d_in) return LF_ERR_INVALID_ARG;
-        if ((q.x_ld & 7) || !aligned16(q.base)) return LF_ERR_ALIGNMENT;
-        MixProj& t = A.p[p];
-        mix_tables(t, q.slice, q.d_in);
-        t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
-        t.in2 = reinterpret_cast<const __nv_bfloat16*>(q.base);
-        t.out = reinterpret_cast<__nv_bfloat16*>(q.y);
-        t.x_ld = q.x_ld;
-        t.out_ld = q.y_ld;
+        const lf_status ps = mix_projection(projs[p], A.p[p]);
+        if (ps != LF_OK) return ps;
     }
-    (void)ws;
-    (void)ws_bytes;
-    return launch_mixture_token<false>(A, reinterpret_cast<cudaStream_t>(stream));
+    const size_t need = mix_ws_size(T, top_k, n_adapters, projs, n_proj, false);
+    if (need > 0 && !ws) return LF_ERR_INVALID_ARG;
+    if (ws_bytes < need) return LF_ERR_WORKSPACE;
+    return mix_run<false>(A, nullptr, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids, const float* weights,
@@ -2279,37 +2469,24 @@ lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids,
     A.scales = adapter_scale;
     bool any = grad_weights != nullptr;
     for (int p = 0; p < n_proj; ++p) {
-        const lf_mixture_grad& q = projs[p];
-        if (q.reserved != 0) return LF_ERR_INVALID_ARG;
-        const lf_status cs = check_apply(q.d_in, q.x, q.dy, q.dy_ld, &q.slice, 1, false);
-        if (cs != LF_OK) return cs;
-        if (q.x_ld < q.d_in || (q.dx && q.dx_ld < q.d_in) || (q.dx_base && !q.dx)) return LF_ERR_INVALID_ARG;
-        if ((q.x_ld & 7) || (q.dx && (q.dx_ld & 7)) || !aligned16(q.dx) || !aligned16(q.dx_base)) return LF_ERR_ALIGNMENT;
-        any = any || q.dx;
-        MixProj& t = A.p[p];
-        mix_tables(t, q.slice, q.d_in);
-        t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
-        t.in2 = reinterpret_cast<const __nv_bfloat16*>(q.dy);
-        t.base = reinterpret_cast<const __nv_bfloat16*>(q.dx_base);
-        t.out = reinterpret_cast<__nv_bfloat16*>(q.dx);
-        t.x_ld = q.x_ld;
-        t.dy_ld = q.dy_ld;
-        t.out_ld = q.dx_ld;
+        const lf_status ps = mix_projection(projs[p], A.p[p]);
+        if (ps != LF_OK) return ps;
+        any = any || projs[p].dx;
     }
     if (!any) return LF_OK;
+    const size_t need = mix_ws_size(T, top_k, n_adapters, projs, n_proj, true);
+    if (need > 0 && !ws) return LF_ERR_INVALID_ARG;
+    if (ws_bytes < need) return LF_ERR_WORKSPACE;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool sum = grad_weights && n_proj > 1;
-    if (sum) {
-        if (!ws) return LF_ERR_INVALID_ARG;
-        if (ws_bytes < mix_ws_bytes(T, top_k, n_proj)) return LF_ERR_WORKSPACE;
-        A.gw = reinterpret_cast<float*>(align_up((int64_t)reinterpret_cast<uintptr_t>(ws), 256));
-    } else {
-        A.gw = grad_weights;
-    }
-    const lf_status ls = launch_mixture_token<true>(A, s);
-    if (ls != LF_OK || !sum) return ls;
+    if (!grad_weights || n_proj == 1) return mix_run<true>(A, grad_weights, ws, s);
+    // the projections' shares of the weights' gradient at the end of the workspace, then their sum
     const int64_t n = (int64_t)T * top_k;
-    LF_LAUNCH("mixture_gw_sum", mixture_gw_sum_kernel, (unsigned)cdiv(n, 256), 256, 0, s, A.gw, n_proj, n, grad_weights);
+    const size_t part = (size_t)n * n_proj * sizeof(float) + 512;
+    float* gw = reinterpret_cast<float*>(
+        align_up((int64_t)reinterpret_cast<uintptr_t>(reinterpret_cast<char*>(ws) + (need - part)), 256));
+    const lf_status ls = mix_run<true>(A, gw, ws, s);
+    if (ls != LF_OK) return ls;
+    LF_LAUNCH("mixture_gw_sum", mixture_gw_sum_kernel, (unsigned)cdiv(n, 256), 256, 0, s, gw, n_proj, n, grad_weights);
     return launch_status();
 }
 

@@ -41,6 +41,22 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(const void* p) {
     return d;
 }
 
+// Shared-memory matrix descriptor of an MN-major bf16 operand in the 128-byte swizzle layout,
+// as 2-D TMA loads with a 64-element inner box along MN write it: K row r of a piece of 64 MN
+// elements at r * 128 bytes (16-byte chunks XOR-permuted by r % 8), groups of 8 K rows 1024
+// bytes apart (the SBO), the next piece of 64 MN elements `piece_bytes` further (the LBO).  A
+// K = 16 step starts 2048 bytes after the last.
+__device__ __forceinline__ uint64_t smem_desc_sw128_mn(const void* p, uint32_t piece_bytes) {
+    const uint64_t addr = smem_u32(p);
+    uint64_t d = 0;
+    d |= (addr >> 4) & 0x3FFFull;
+    d |= (uint64_t)((piece_bytes >> 4) & 0x3FFFu) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= 1ull << 46;                        // descriptor version for sm_100
+    d |= 2ull << 61;                        // layout type: 128-byte swizzle
+    return d;
+}
+
 // 2-D tiled TMA load (no multicast) of the tensor map's box at coordinates (c0 =
 // innermost, c1) into this CTA's shared memory; completion is counted in bytes on
 // `bar`.  c0 * element size must be a multiple of 16 bytes; rows or columns outside the
@@ -122,7 +138,16 @@ __device__ __forceinline__ void mma_bf16_ta_warp(uint32_t d_tmem, uint32_t a_tme
         "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
         : "memory");
 }
-// The commit of the lane that mma_bf16_ta_warp elects.
+// The same with A in shared memory.
+__device__ __forceinline__ void mma_bf16_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                              bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\telect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+        : "memory");
+}
+// The commit of the lane that these elect.
 __device__ __forceinline__ void commit_warp(uint64_t* bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
@@ -207,6 +232,18 @@ __device__ __forceinline__ void tmem_ld8x6(const uint32_t (&ta)[6], int32_t (&v)
 // Barrier among `nthreads` threads (whole warps) on hardware barrier `id` (1..15).
 __device__ __forceinline__ void named_sync(int id, int nthreads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+
+// The same, returning whether `pred` holds in every thread.
+__device__ __forceinline__ bool named_sync_and(int id, int nthreads, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %3, 0;\n\tbarrier.cta.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}\n"
+        : "=r"(r)
+        : "r"(id), "r"(nthreads), "r"((uint32_t)pred)
+        : "memory");
+    return r != 0;
 }
 
 // 16-byte asynchronous global -> shared copy (generic proxy) and its group fences.

@@ -184,7 +184,9 @@ def lib() -> ctypes.CDLL:
         L.lf_route_experts.restype = ctypes.c_int
         L.lf_route_experts_backward.argtypes = [_I32, _P, _P, _I32, _I64, _P, _P, _P, _I64, _P]
         L.lf_route_experts_backward.restype = ctypes.c_int
-        L.lf_lora_mixture_workspace_size.argtypes = [_I32] * 5; L.lf_lora_mixture_workspace_size.restype = _SZ
+        for f in (L.lf_lora_mixture_workspace_size, L.lf_lora_mixture_backward_workspace_size):
+            f.argtypes = [_I32, _I32, _I32, _P, _I32]
+            f.restype = _SZ
         L.lf_lora_mixture.argtypes = [_I32, _I32, _P, _P, _I32, _P, _I32, _F, _P, _P, _SZ, _P]
         L.lf_lora_mixture.restype = ctypes.c_int
         L.lf_lora_mixture_backward.argtypes = [_I32, _I32, _P, _P, _I32, _P, _I32, _F, _P, _P, _P, _SZ, _P]
@@ -213,7 +215,7 @@ def exported_symbols() -> list[str]:
             "lf_lora_sigma_sandwich", "lf_jd_workspace_size", "lf_jd_full", "lf_route_tokens",
             "lf_lora_shrink_expand_slices_routed", "lf_check_bounded_wait", "lf_pool_workspace_size",
             "lf_pool_subspace", "lf_lora_shrink_expand_projections", "lf_route_experts", "lf_route_experts_backward",
-            "lf_lora_mixture_workspace_size", "lf_lora_mixture", "lf_lora_mixture_backward", "lf_w4_quantize",
+            "lf_lora_mixture_workspace_size", "lf_lora_mixture_backward_workspace_size", "lf_lora_mixture", "lf_lora_mixture_backward", "lf_w4_quantize",
             "lf_w4_dequantize", "lf_w4_workspace_size", "lf_w4_projections"]
 
 # Limits of lf_lora_shrink_expand_noalloc (its scratch is a fixed array in the library).
@@ -454,8 +456,14 @@ def make_mixture_grad(x, dy, dx, sl: lf_slice, dx_base=None) -> lf_mixture_grad:
     return p
 
 
-def lf_lora_mixture_workspace_size(T: int, top_k: int, n_adapters: int, n_proj: int, max_rank: int = 0) -> int:
-    return lib().lf_lora_mixture_workspace_size(T, top_k, n_adapters, n_proj, max_rank)
+def lf_lora_mixture_workspace_size(T: int, top_k: int, n_adapters: int, projections) -> int:
+    arr = (lf_mixture_projection * len(projections))(*projections)
+    return lib().lf_lora_mixture_workspace_size(T, top_k, n_adapters, arr, len(projections))
+
+
+def lf_lora_mixture_backward_workspace_size(T: int, top_k: int, n_adapters: int, grads) -> int:
+    arr = (lf_mixture_grad * len(grads))(*grads)
+    return lib().lf_lora_mixture_backward_workspace_size(T, top_k, n_adapters, arr, len(grads))
 
 
 def lf_lora_mixture(ids, weights, n_adapters, projections, scale, ws=None, adapter_scale=None, stream=None,

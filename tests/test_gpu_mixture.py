@@ -78,6 +78,9 @@ SHAPES = [
     (37, 8, 2, 520, 264, 33), (64, 16, 2, 512, 1024, 16), (150, 40, 4, 256, 248, 9), (333, 5, 2, 264, 520, 64),
     (700, 12, 2, 1024, 384, 16), (1025, 9, 3, 200, 136, 7), (40, 2, 16, 64, 64, 64), (600, 64, 2, 320, 512, 16),
     (300, 3, 1, 4096, 128, 8),
+    # long batches over small pools (dense products over the stacked rows: up to 256, 512, 768, 1024)
+    (1111, 16, 6, 1544, 2056, 16), (700, 12, 2, 2048, 1992, 64), (2000, 16, 4, 1032, 1304, 64), (300, 3, 16, 4096, 1024, 64),
+    (513, 130, 8, 4096, 2048, 7), (640, 8, 3, 5000, 40, 32), (257, 4, 8, 64, 6008, 64),
 ]
 
 
@@ -103,40 +106,43 @@ def test_forward_and_backward(T, E, K, d_in, d_out, mr):
         assert lf.lf_get_device_status() == 0
 
 
-@pytest.mark.parametrize("T", [3, 260])
-def test_strides_offsets_scales_in_place(T):
+# token by token, and long enough over a small pool for the dense products
+@pytest.mark.parametrize("T,K,d_in,d_out,mr", [(3, 2, 264, 392, 24), (260, 2, 264, 392, 24), (260, 8, 1288, 1544, 64)])
+def test_strides_offsets_scales_in_place(T, K, d_in, d_out, mr):
     """x, y and dx as column windows of wider tensors, a slice inside y, per-adapter scales, y
     and dx updated in place; everything outside the window keeps its bits."""
-    b = Batch(T, 6, 2, 264, 392, 24, seed=5, pad=40)
+    b = Batch(T, 6, K, d_in, d_out, mr, seed=5, pad=40)
     D = b.dev()
     sc = np.array([0.5, 2.0, -1.0, 0.0, 3.0, 1.5], np.float32)
     scd = torch.from_numpy(sc).cuda()
-    x = D["x"][:, 16:16 + 264]
+    x = D["x"][:, 16:16 + d_in]
     y = D["base"].clone()
     sl = b.slice(D, y_off=24)
     api.lora_mixture(D["ids"], D["w"], 6, [lf.make_mixture_projection(x, y, sl, base=y)], 9.0, adapter_scale=scd)
-    xn = b.x.float().numpy()[:, 16:280]
+    xn = b.x.float().numpy()[:, 16:16 + d_in]
     bn = b.base.float().numpy()
-    want, mag = OR.mixture(xn, bn[:, 24:24 + 392], b.ids, b.w, *b.pools(), 9.0, sc)
-    check(y[:, 24:24 + 392], want, mag, 264 + b.R + 8)
-    assert torch.equal(y[:, :24], D["base"][:, :24]) and torch.equal(y[:, 416:], D["base"][:, 416:])
+    want, mag = OR.mixture(xn, bn[:, 24:24 + d_out], b.ids, b.w, *b.pools(), 9.0, sc)
+    check(y[:, 24:24 + d_out], want, mag, d_in + b.R + 8)
+    assert torch.equal(y[:, :24], D["base"][:, :24]) and torch.equal(y[:, 24 + d_out:], D["base"][:, 24 + d_out:])
     idle = torch.from_numpy((b.ids < 0).all(axis=1)).cuda()
     assert torch.equal(y[idle], D["base"][idle])
     dx_all = D["dxb"].clone()
-    dx = dx_all[:, 8:8 + 264]
+    dx = dx_all[:, 8:8 + d_in]
     gw = api.lora_mixture_backward(D["ids"], D["w"], 6, [lf.make_mixture_grad(x, D["dy"], dx, sl, dx_base=dx)], 9.0,
                                    adapter_scale=scd)
-    dxr, dxm, dwr, dwm = OR.mixture_grad(xn, b.dy.float().numpy()[:, 24:416], b.ids, b.w, *b.pools(), 9.0, sc)
-    base = b.dxb.float().numpy()[:, 8:272].astype(np.float64)
-    check(dx, dxr + base, dxm + np.abs(base), 392 + b.R + 8)
-    assert torch.equal(dx_all[:, :8], D["dxb"][:, :8]) and torch.equal(dx_all[:, 272:], D["dxb"][:, 272:])
-    assert (np.abs(gw.double().cpu().numpy() - dwr) <= (264 + 392 + 32) * 2.0 ** -24 * dwm + 1e-37).all()
+    dxr, dxm, dwr, dwm = OR.mixture_grad(xn, b.dy.float().numpy()[:, 24:24 + d_out], b.ids, b.w, *b.pools(), 9.0, sc)
+    base = b.dxb.float().numpy()[:, 8:8 + d_in].astype(np.float64)
+    check(dx, dxr + base, dxm + np.abs(base), d_out + b.R + 8)
+    assert torch.equal(dx_all[:, :8], D["dxb"][:, :8]) and torch.equal(dx_all[:, 8 + d_in:], D["dxb"][:, 8 + d_in:])
+    assert (np.abs(gw.double().cpu().numpy() - dwr) <= (d_in + d_out + mr + 8) * 2.0 ** -24 * dwm + 1e-37).all()
     assert lf.lf_get_device_status() == 0
 
 
-@pytest.mark.parametrize("T", [2, 300])
-def test_several_projections_share_the_weights_gradient(T):
-    bs = [Batch(T, 7, 2, 128, 64, 16, seed=1), Batch(T, 7, 2, 256, 520, 5, seed=2), Batch(T, 7, 2, 8, 128, 8, seed=3)]
+@pytest.mark.parametrize("T,big", [(2, False), (300, False), (700, True)])
+def test_several_projections_share_the_weights_gradient(T, big):
+    """big: the second projection is wide enough for the dense products, the others are not."""
+    d1, d2, r = (2048, 2056, 64) if big else (256, 520, 5)
+    bs = [Batch(T, 7, 2, 128, 64, 16, seed=1), Batch(T, 7, 2, d1, d2, r, seed=2), Batch(T, 7, 2, 8, 128, 8, seed=3)]
     Ds = [b.dev() for b in bs]
     for b in bs:
         b.ids, b.w = bs[0].ids, bs[0].w
@@ -155,7 +161,7 @@ def test_several_projections_share_the_weights_gradient(T):
         if dx is not None:
             check(dx, dxr, dxm, b.d_out + b.R + 8)
         tot, totm = tot + dwr, totm + dwm
-    assert (np.abs(gw.double().cpu().numpy() - tot) <= (256 + 520 + 32) * 2.0 ** -24 * totm + 1e-37).all()
+    assert (np.abs(gw.double().cpu().numpy() - tot) <= (d1 + d2 + r + 32) * 2.0 ** -24 * totm + 1e-37).all()
     # the weights' gradient alone, and dx alone
     g2 = api.lora_mixture_backward(ids, w, 7, [lf.make_mixture_grad(D["x"], D["dy"], None, b.slice(D))
                                                for b, D in zip(bs, Ds)], 1.0)
@@ -167,9 +173,9 @@ def test_several_projections_share_the_weights_gradient(T):
     assert lf.lf_get_device_status() == 0
 
 
-@pytest.mark.parametrize("T", [4, 400])
-def test_bad_ids_and_factors_leave_only_their_slots_out(T):
-    b = Batch(T, 6, 3, 64, 128, 12, seed=8, empty=0.0, ranks=[4, 70, 3, 5, 6, 7])
+@pytest.mark.parametrize("T,d_in,d_out", [(4, 64, 128), (400, 64, 128), (900, 2048, 1096)])
+def test_bad_ids_and_factors_leave_only_their_slots_out(T, d_in, d_out):
+    b = Batch(T, 6, 3, d_in, d_out, 12, seed=8, empty=0.0, ranks=[4, 70, 3, 5, 6, 7])
     b.ids = np.tile(np.array([0, 2, 3], np.int32), (T, 1))
     b.ids[0] = [0, 6, 3]                # out of range
     ref = b.ids.copy()
@@ -184,7 +190,7 @@ def test_bad_ids_and_factors_leave_only_their_slots_out(T):
     assert lf.lf_get_device_status() == 3
     xn, bn = b.x.float().numpy(), b.base.float().numpy()
     want, mag = OR.mixture(xn, bn, ref, b.w, *b.pools(), 1.0)
-    check(y, want, mag, 64 + 64 + 8)
+    check(y, want, mag, d_in + 64 + 8)
     gw = api.lora_mixture_backward(D["ids"], D["w"], 6, [lf.make_mixture_grad(D["x"], D["dy"], None, b.slice(D))], 1.0)
     assert lf.lf_get_device_status() == 3 and float(gw[0, 1]) == 0.0
     # a rank above 64 (adapter 1) and an offset past the pool (adapter 2)
@@ -195,10 +201,10 @@ def test_bad_ids_and_factors_leave_only_their_slots_out(T):
     ref = b.ids.copy()
     ref[:, 1] = -1
     want, mag = OR.mixture(xn, bn, ref, b.w, *b.pools(), 1.0)
-    check(y, want, mag, 64 + 64 + 8)
+    check(y, want, mag, d_in + 64 + 8)
     b.ids = np.tile(np.array([0, 2, 3], np.int32), (T, 1))
     keep = b.offA[2]
-    b.offA[2] = b.A.numel() - 64
+    b.offA[2] = b.A.numel() - d_in
     D = b.dev()
     y = y_of(D)
     assert lf.lf_get_device_status() == 4
@@ -206,29 +212,46 @@ def test_bad_ids_and_factors_leave_only_their_slots_out(T):
     ref = b.ids.copy()
     ref[:, 1] = -1
     want, mag = OR.mixture(xn, bn, ref, b.w, *b.pools(), 1.0)
-    check(y, want, mag, 64 + 64 + 8)
+    check(y, want, mag, d_in + 64 + 8)
 
 
-def test_values_that_are_not_finite_stay_in_their_slots():
-    """An infinite weight of an empty slot is not read; NaN in one token's x stays there."""
-    b = Batch(260, 4, 2, 64, 64, 8, seed=4, ranks=[8, 8, 8, 8])
+@pytest.mark.parametrize("T,K,d_in,d_out", [(260, 2, 64, 64), (800, 4, 2048, 1544)])
+def test_values_that_are_not_finite_stay_in_their_tokens(T, K, d_in, d_out):
+    """An infinite weight of an empty slot is not read; NaN in one token's x stays there; factors
+    that are not finite reach only the tokens that use them."""
+    b = Batch(T, 8, K, d_in, d_out, 64, seed=4, ranks=[64, 8, 8, 64, 64, 8, 8, 8])
+    b.ids[b.ids == 7] = -1               # adapter 7 is used by no token
+    b.ids[(b.ids == 6) & (np.arange(T)[:, None] % 50 != 0)] = 5
     b.w[b.ids < 0] = np.inf
+    b.A[b.offA[7]:b.offA[7] + 100] = float("nan")
+    b.Bt[b.offB[7] + 3] = float("inf")
+    b.Bt[b.offB[6] + d_out + 5] = float("nan")
     D = b.dev()
     D["x"][7] = float("nan")
-    y = torch.empty_like(D["base"])
-    api.lora_mixture(D["ids"], D["w"], 4, [lf.make_mixture_projection(D["x"], y, b.slice(D, max_rank=8), base=D["base"])], 1.0)
-    ok = torch.isfinite(y).all(dim=1)
-    assert ok.sum() >= 259 and (not ok[7] or (b.ids[7] < 0).all())
+    y, dx = torch.empty_like(D["base"]), torch.empty_like(D["x"])
+    sl = b.slice(D)
+    api.lora_mixture(D["ids"], D["w"], 8, [lf.make_mixture_projection(D["x"], y, sl, base=D["base"])], 1.0)
+    gw = api.lora_mixture_backward(D["ids"], D["w"], 8, [lf.make_mixture_grad(D["x"], D["dy"], dx, sl)], 1.0)
+    uses6 = torch.from_numpy((b.ids == 6).any(axis=1)).cuda()
+    clean = ~uses6
+    clean[7] = False
+    assert torch.isfinite(y[clean]).all() and torch.isfinite(dx[clean]).all() and torch.isfinite(gw[clean]).all()
+    assert torch.isnan(y[uses6]).any(dim=1).all() and torch.isnan(dx[uses6]).any(dim=1).all()
+    assert torch.isnan(gw[torch.from_numpy(b.ids == 6).cuda()]).all()
+    assert not torch.isfinite(y[7]).all() or (b.ids[7] < 0).all()
     assert lf.lf_get_device_status() == 0
 
 
-def test_same_results_from_run_to_run_and_captured():
-    b = Batch(512, 16, 2, 512, 512, 16, seed=6)
+@pytest.mark.parametrize("K,d_in,d_out", [(2, 512, 512), (4, 2048, 2048)])
+def test_same_results_from_run_to_run_and_captured(K, d_in, d_out):
+    b = Batch(512, 16, K, d_in, d_out, 64, seed=6)
     D = b.dev()
-    sl = b.slice(D, max_rank=16)
-    ws = api.workspace(max(1, lf.lf_lora_mixture_workspace_size(512, 2, 16, 1, 16)), "cuda")
+    sl = b.slice(D)
     y, dx = torch.empty_like(D["base"]), torch.empty_like(D["x"])
-    gw = torch.empty(512, 2, device="cuda")
+    gw = torch.empty(512, K, device="cuda")
+    ws = api.workspace(max(lf.lf_lora_mixture_workspace_size(512, K, 16, [lf.make_mixture_projection(D["x"], y, sl, base=D["base"])]),
+                           lf.lf_lora_mixture_backward_workspace_size(512, K, 16, [lf.make_mixture_grad(D["x"], D["dy"], dx, sl)])),
+                       "cuda")
 
     def call():
         lf.lf_lora_mixture(D["ids"], D["w"], 16, [lf.make_mixture_projection(D["x"], y, sl, base=D["base"])], 1.0, ws)
@@ -252,11 +275,11 @@ def test_same_results_from_run_to_run_and_captured():
     torch.cuda.synchronize()
     assert all(torch.equal(a, c) for a, c in zip(first, (y, dx, gw)))
     # new ids through the same graph
-    b2 = Batch(512, 16, 2, 512, 512, 16, seed=60)
+    b2 = Batch(512, 16, K, d_in, d_out, 64, seed=60)
     D["ids"].copy_(torch.from_numpy(b2.ids))
     gr.replay()
     want, mag = OR.mixture(b.x.float().numpy(), b.base.float().numpy(), b2.ids, b.w, *b.pools(), 1.0)
-    check(y, want, mag, 512 + b.R + 8)
+    check(y, want, mag, d_in + b.R + 8)
     assert lf.lf_get_device_status() == 0
 
 
@@ -265,8 +288,8 @@ def test_empty_batch_and_module_of_zero_ranks():
     D = b.dev()
     y = torch.empty_like(D["base"])
     api.lora_mixture(D["ids"], D["w"], 3, [lf.make_mixture_projection(D["x"], y, b.slice(D))], 1.0)
-    for T in (3, 300):
-        b = Batch(T, 3, 2, 64, 64, 4, seed=1, ranks=[0, 0, 0])
+    for T, d in ((3, 64), (300, 64), (1500, 2048)):
+        b = Batch(T, 3, 8, d, d, 4, seed=1, ranks=[0, 0, 0])
         D = b.dev()
         y = torch.empty_like(D["base"])
         api.lora_mixture(D["ids"], D["w"], 3, [lf.make_mixture_projection(D["x"], y, b.slice(D), base=D["base"])], 1.0)
