@@ -1193,15 +1193,13 @@ static size_t mix_ws_size(int32_t T, int32_t K, int32_t n_adapters, const P* pro
     return most;
 }
 
-static lf_status launch_mix_shrink(const MixShrinkArgs& a, int Rmax, const CUtensorMap& xmap, const CUtensorMap& amap,
-                                   cudaStream_t s) {
-    const int tiles = (int)cdiv(a.T, kMtM), chunks = (int)cdiv(Rmax, kMtN), steps = (int)cdiv(a.d, kMtKB);
-    int cs = 1;   // shares of d: as many CTAs as SMs, four stages or more each
-    while (cs < 8 && 2 * cs * tiles * chunks <= 148 && steps >= 8 * cs) cs *= 2;
-    constexpr size_t sm = sizeof(MixShrinkSmem);
-    LF_CUDA_TRY(cudaFuncSetAttribute(mixture_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
+template <int NCH>
+static lf_status launch_mix_shrink_n(const MixShrinkArgs& a, int Rmax, int cs, const CUtensorMap& xmap,
+                                     const CUtensorMap& amap, cudaStream_t s) {
+    constexpr size_t sm = sizeof(MixShrinkSmem<NCH>);
+    LF_CUDA_TRY(cudaFuncSetAttribute(mixture_shrink_kernel<NCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(tiles * cs), (unsigned)chunks);
+    cfg.gridDim = dim3((unsigned)(cdiv(a.T, kMtM) * cs), (unsigned)cdiv(Rmax, NCH));
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = sm;
     cfg.stream = s;
@@ -1213,8 +1211,18 @@ static lf_status launch_mix_shrink(const MixShrinkArgs& a, int Rmax, const CUten
     cfg.attrs = at;
     cfg.numAttrs = 1;
     PhaseScope ps("mixture_shrink", s);
-    LF_CUDA_TRY(cudaLaunchKernelEx(&cfg, mixture_shrink_kernel, a, xmap, amap));
+    LF_CUDA_TRY(cudaLaunchKernelEx(&cfg, mixture_shrink_kernel<NCH>, a, xmap, amap));
     return LF_OK;
+}
+static lf_status launch_mix_shrink(const MixShrinkArgs& a, int Rmax, const CUtensorMap& xmap, const CUtensorMap& amap,
+                                   cudaStream_t s) {
+    const int64_t tiles = cdiv(a.T, kMtM), steps = cdiv(a.d, kMtKB);
+    // chunks of 128 rows when even eight shares of d leave SMs idle with 256
+    const bool narrow = Rmax <= 128 || tiles * cdiv(Rmax, 256) * 8 < 148;
+    const int64_t chunks = cdiv(Rmax, narrow ? 128 : 256);
+    int cs = 1;   // shares of d: as many CTAs as SMs, eight stages or more each
+    while (cs < 8 && 2 * cs * tiles * chunks <= 148 && steps >= 16 * cs) cs *= 2;
+    return narrow ? launch_mix_shrink_n<128>(a, Rmax, cs, xmap, amap, s) : launch_mix_shrink_n<256>(a, Rmax, cs, xmap, amap, s);
 }
 
 // One projection on the dense path.  grad: P is a gradient's table (in2 = dy, out = dx).
@@ -1225,10 +1233,10 @@ static lf_status mix_dense_projection(const MixArgs& A, const MixProj& P, bool g
     MixTcWs w;
     carve_mix(reinterpret_cast<char*>(align_up((int64_t)reinterpret_cast<uintptr_t>(ws), 256)), T, Rp, P.d_in, P.d_out, grad, &w);
     alignas(64) CUtensorMap xm, dym, am, bm, ab, bb, him, lom, basem, outm;
-    bool ok = encode_x_map(&xm, P.x, A.T, P.d_in, P.x_ld, kMtM) && encode_x_map(&am, w.A, Rp, P.d_in, P.d_in, kMtN) &&
+    bool ok = encode_x_map(&xm, P.x, A.T, P.d_in, P.x_ld, kMtM) && encode_x_map(&am, w.A, Rp, P.d_in, P.d_in, kMtABox) &&
               encode_x_map(&him, w.hi, A.T, Rp, Rp, kMtM) && encode_x_map(&lom, w.lo, A.T, Rp, Rp, kMtM);
     if (grad) ok = ok && encode_x_map(&dym, P.in2 + P.y_off, A.T, P.d_out, P.dy_ld, kMtM) &&
-                   encode_x_map(&bm, w.Bt, Rp, P.d_out, P.d_out, kMtN);
+                   encode_x_map(&bm, w.Bt, Rp, P.d_out, P.d_out, kMtABox);
     const bool expand = !grad || P.out;
     const int dout = grad ? P.d_in : P.d_out;   // columns the expand writes
     const __nv_bfloat16* base = grad ? P.base : (P.in2 ? P.in2 + P.y_off : nullptr);

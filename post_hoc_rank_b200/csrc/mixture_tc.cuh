@@ -158,42 +158,51 @@ struct MixShrinkArgs {
     __nv_bfloat16* lo;
 };
 
-constexpr int kMtShrinkStages = 4;
+constexpr int mt_shrink_stages(int nch) { return nch == 128 ? 6 : 4; }
+constexpr int kMtABox = 32;        // stacked rows per copy: a chunk loads what it has, rounded up to this
+template <int NCH>
 struct MixShrinkSmem {
+    static constexpr int kMtShrinkStages = mt_shrink_stages(NCH);
     union {
         struct {
             unsigned char x[kMtShrinkStages][kMtM * 128];
-            unsigned char a[kMtShrinkStages][kMtN * 128];
+            unsigned char a[kMtShrinkStages][NCH * 128];
         };
-        float part[kMtM][kMtN + 4];
+        float part[kMtM][NCH + 4];
     };
-    int32_t expert[kMtN], bad[kMtN];
-    int32_t ids[kMtM][kMixMaxK];
+    int32_t bad[NCH];
+    // the tokens' slots: first stacked row of the expert less r0, its rank (0: nothing), weight
+    // times scale; an expert named twice has one slot with the sum of its weights
+    int16_t col[kMtM][kMixMaxK], rank[kMtM][kMixMaxK];
     float w[kMtM][kMixMaxK];
     uint64_t full[kMtShrinkStages], empty[kMtShrinkStages], done;
     uint32_t tmem;
     int32_t failed;
 };
 
-// xmap: T rows of d columns, box 64 x 128; amap: Rp rows of d columns, box 64 x 256; 128-byte
-// swizzle both.  Grid: clusters of CS along x (shares of d), token tiles, y = chunks of 256 rows.
-// Warp 0 issues the copies, warp 1 the products; all eight form the sums.
+// xmap: T rows of d columns, box 64 x 128; amap: Rp rows of d columns, box 64 x 32; 128-byte
+// swizzle both.  Grid: clusters of CS along x (shares of d), token tiles, y = chunks of NCH rows.
+// Warp 0 issues the copies, warp 1 the products; all eight form the sums.  NCH 256: x is read
+// once for 256 rows; 128: twice the CTAs, where 256 leave most SMs idle.
+template <int NCH>
 __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_constant__ MixShrinkArgs a,
                                                                 const __grid_constant__ CUtensorMap xmap,
                                                                 const __grid_constant__ CUtensorMap amap) {
     namespace cg = cooperative_groups;
+    constexpr int kMtShrinkStages = mt_shrink_stages(NCH);
     extern __shared__ __align__(1024) unsigned char mt_raw[];
-    auto& s = *reinterpret_cast<MixShrinkSmem*>(mt_raw);
+    auto& s = *reinterpret_cast<MixShrinkSmem<NCH>*>(mt_raw);
     cg::cluster_group cl = cg::this_cluster();
     const int CS = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-    const int tok0 = ((int)blockIdx.x / CS) * kMtM, r0 = blockIdx.y * kMtN;
+    const int tok0 = ((int)blockIdx.x / CS) * kMtM, r0 = blockIdx.y * NCH;
     const int R = a.plan->R;
     if (r0 >= ((R + kMtKB - 1) & ~(kMtKB - 1)) && r0 > 0) return;   // uniform over the cluster: no rows here
-    const int n = min(kMtN, (max(R - r0, 1) + 15) & ~15);    // rows of this chunk, for the products
+    const int n = min(NCH, (max(R - r0, 1) + 15) & ~15);     // rows of this chunk, for the products
+    const int nbox = (n + kMtABox - 1) / kMtABox;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int steps = (a.d + kMtKB - 1) / kMtKB;
     const int k0 = (int)((int64_t)steps * rank / CS), nk = (int)((int64_t)steps * (rank + 1) / CS) - k0;
-    if (warp == 0) tc::tmem_alloc(&s.tmem, kMtN);
+    if (warp == 0) tc::tmem_alloc(&s.tmem, NCH);
     if (tid == 0) {
         for (int i = 0; i < kMtShrinkStages; ++i) {
             mbar_init(&s.full[i], 1);
@@ -203,32 +212,51 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
         s.failed = 0;
         fence_barrier_init();
     }
-    {
+    if (tid < NCH) {
         const int r = min(r0 + tid, a.Rp - 1);
-        s.expert[tid] = a.plan->expert[r];
         s.bad[tid] = a.plan->bad[0][r] | a.plan->bad[1][r];
-    }
-    if (a.hi || a.report) {   // the tile's slots: id (or -1) and weight times scale
-        for (int i = tid; i < kMtM * a.K; i += 256) {
-            const int m = i / a.K, j = i - m * a.K, t = tok0 + m;
-            int id = t < a.T ? a.ids[(int64_t)t * a.K + j] : -1;
-            const bool lead = a.report && r0 == 0 && rank == 0;
-            if (id < -1 || id >= a.n_adapters) {
-                if (lead) latch_error(LF_ERR_BAD_INDEX);
-                id = -1;
-            } else if (id >= 0 && a.plan->rank[id] == 0) {
-                if (lead && a.plan->err[id]) latch_error(a.plan->err[id]);
-                id = -1;
-            }
-            s.ids[m][j] = id;
-            s.w[m][j] = id < 0 ? 0.f : (a.weights ? a.weights[(int64_t)t * a.K + j] : 1.f) * (a.scales ? a.scales[id] : a.scale);
-        }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
     const uint32_t tmem = s.tmem;
     bool ok = true;
+    if (warp >= 4) {   // a thread per token: its slots, while the products run
+        const int m = tid - 128, t = tok0 + m;
+        const bool lead = a.report && r0 == 0 && rank == 0;
+        if ((a.hi || lead) && t < a.T) {
+            int id[kMixMaxK];
+#pragma unroll
+            for (int j = 0; j < kMixMaxK; ++j) {
+                id[j] = j < a.K ? a.ids[(int64_t)t * a.K + j] : -1;
+                if (id[j] < -1 || id[j] >= a.n_adapters) {
+                    if (lead) latch_error(LF_ERR_BAD_INDEX);
+                    id[j] = -1;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kMixMaxK; ++j) {
+                if (j >= a.K) break;
+                int k = 0, c = 0;
+                float w = 0.f;
+                if (id[j] >= 0) {
+                    k = a.plan->rank[id[j]];
+                    c = a.plan->first[id[j]] - r0;
+                    if (k == 0 && lead && a.plan->err[id[j]]) latch_error(a.plan->err[id[j]]);
+                    w = (a.weights ? a.weights[(int64_t)t * a.K + j] : 1.f) * (a.scales ? a.scales[id[j]] : a.scale);
+#pragma unroll
+                    for (int q = 0; q < kMixMaxK; ++q)   // into the expert's first slot
+                        if (q < j && id[q] == id[j] && k > 0) {
+                            s.w[m][q] += w;
+                            k = 0;
+                        }
+                }
+                s.col[m][j] = (int16_t)c;
+                s.rank[m][j] = (int16_t)k;
+                s.w[m][j] = w;
+            }
+        }
+    }
     if (warp == 0) {
         if (lane == 0) {
             int i = 0;
@@ -236,9 +264,10 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
                 const int st = i % kMtShrinkStages;
                 if (i >= kMtShrinkStages) ok = mbar_wait(&s.empty[st], (uint32_t)(i / kMtShrinkStages - 1) & 1);
                 if (!ok) break;
-                mbar_arrive_expect_tx(&s.full[st], (kMtM + kMtN) * 128);
+                mbar_arrive_expect_tx(&s.full[st], (kMtM + nbox * kMtABox) * 128);
                 tc::tma_load_2d(s.x[st], &xmap, (k0 + i) * kMtKB, tok0, &s.full[st]);
-                tc::tma_load_2d(s.a[st], &amap, (k0 + i) * kMtKB, r0, &s.full[st]);
+                for (int q = 0; q < nbox; ++q)
+                    tc::tma_load_2d(s.a[st] + q * kMtABox * 128, &amap, (k0 + i) * kMtKB, r0 + q * kMtABox, &s.full[st]);
             }
             // nothing is in flight when the buffers are reused or the CTA leaves
             for (int j = max(0, i - kMtShrinkStages); j < i; ++j)
@@ -253,7 +282,7 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
             ok = __all_sync(0xffffffffu, mbar_wait(&s.full[st], (uint32_t)(i / kMtShrinkStages) & 1));
             if (!ok) break;
             tc::fence_after_sync();
-            const uint64_t xd = xd0 + (uint64_t)(st * (kMtM * 128 / 16)), ad = ad0 + (uint64_t)(st * (kMtN * 128 / 16));
+            const uint64_t xd = xd0 + (uint64_t)(st * (kMtM * 128 / 16)), ad = ad0 + (uint64_t)(st * (NCH * 128 / 16));
 #pragma unroll
             for (int k = 0; k < kMtKB / 16; ++k) tc::mma_bf16_warp(tm, xd + 2 * k, ad + 2 * k, idesc, i > 0 || k > 0);
             tc::commit_warp(&s.empty[st]);
@@ -268,8 +297,8 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
     __syncthreads();   // all products complete, all copies landed: the stages become the partial sums
     tc::fence_after_sync();
     {
-        const int m = 32 * (warp & 3) + lane, c0 = (warp >> 2) * (kMtN / 2);
-        for (int c = c0; c < min(c0 + kMtN / 2, n); c += 16) {
+        const int m = 32 * (warp & 3) + lane, c0 = (warp >> 2) * (NCH / 2);
+        for (int c = c0; c < min(c0 + NCH / 2, n); c += 16) {
             float v[16];
             tc::tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, v);
 #pragma unroll
@@ -281,54 +310,59 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 0) tc::tmem_dealloc(tmem, kMtN);
+    if (warp == 0) tc::tmem_dealloc(tmem, NCH);
     if (CS > 1) cl.sync();
     bool all_ok = s.failed == 0;
     for (int c = 0; c < CS && CS > 1; ++c) all_ok = all_ok && *cl.map_shared_rank(&s.failed, c) == 0;
     if (all_ok) {   // uniform over the cluster; a timeout is latched
-        // this CTA's rows of the tile, 256 / rows threads on each, `rows` x 2 columns a thread
-        const int rows = kMtM / CS, tpr = 256 / rows, seg = kMtN / tpr;
-        const int m = rank * rows + tid / tpr, t = tok0 + m;
-        const int c0 = (tid % tpr) * seg;
-        int cur = -2;
-        float coef = 0.f;
-        if (t < a.T) {
-            for (int c = c0; c < min(c0 + seg, min(kMtN, a.Rp - r0)); c += 8) {
-                float v[8];
+        // this CTA's rows of the tile.  Raw sums and the zeros of P first, whole rows at a time;
+        // the loads of a batch of pieces (remote shared memory among them) go out together
+        const int rows = kMtM / CS, m0 = rank * rows;
+        constexpr int V = NCH / 4, kBatch = 4;   // four-column pieces per row
+        for (int i0 = tid; i0 < rows * V; i0 += 256 * kBatch) {
+            float4 v[kBatch];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = 0.f;
-                if (c < n) {
-                    for (int q = 0; q < CS; ++q) {
-                        const float* p = CS > 1 ? cl.map_shared_rank(&s.part[m][c], q) : &s.part[m][c];
-                        const float4 u0 = *reinterpret_cast<const float4*>(p), u1 = *reinterpret_cast<const float4*>(p + 4);
-                        v[0] += u0.x, v[1] += u0.y, v[2] += u0.z, v[3] += u0.w;
-                        v[4] += u1.x, v[5] += u1.y, v[6] += u1.z, v[7] += u1.w;
-                    }
+            for (int u = 0; u < kBatch; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q = 0; q < CS && a.raw; ++q) {
+                float4 p[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const int i = i0 + 256 * u, m = m0 + i / V, c = i % V * 4;
+                    p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (i < rows * V && c < n && tok0 + m < a.T)
+                        p[u] = *reinterpret_cast<const float4*>(CS > 1 ? cl.map_shared_rank(&s.part[m][c], q) : &s.part[m][c]);
                 }
-                const int64_t at = (int64_t)t * a.Rp + r0 + c;
-                if (a.raw) {
-                    *reinterpret_cast<float4*>(a.raw + at) = make_float4(v[0], v[1], v[2], v[3]);
-                    *reinterpret_cast<float4*>(a.raw + at + 4) = make_float4(v[4], v[5], v[6], v[7]);
-                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) v[u].x += p[u].x, v[u].y += p[u].y, v[u].z += p[u].z, v[u].w += p[u].w;
+            }
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const int i = i0 + 256 * u, m = m0 + i / V, c = i % V * 4;
+                if (i >= rows * V || r0 + c >= a.Rp || tok0 + m >= a.T) continue;
+                const int64_t at = (int64_t)(tok0 + m) * a.Rp + r0 + c;
+                if (a.raw) *reinterpret_cast<float4*>(a.raw + at) = v[u];
                 if (a.hi) {
-                    __align__(16) __nv_bfloat16 hi[8], lo[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int e = s.expert[c + i];
-                        if (e != cur) {
-                            cur = e;
-                            coef = 0.f;
-                            if (e >= 0)
-                                for (int j = 0; j < a.K; ++j) coef += s.ids[m][j] == e ? s.w[m][j] : 0.f;
-                        }
-                        // a row outside the token's experts is exactly zero, whatever its sum
-                        const float p = coef == 0.f ? 0.f : (s.bad[c + i] ? NAN : coef * v[i]);
-                        hi[i] = __float2bfloat16_rn(p);
-                        const float h = __bfloat162float(hi[i]);
-                        lo[i] = __float2bfloat16_rn(fabsf(h) < INFINITY ? p - h : 0.f);
-                    }
-                    *reinterpret_cast<uint4*>(a.hi + at) = *reinterpret_cast<const uint4*>(hi);
-                    *reinterpret_cast<uint4*>(a.lo + at) = *reinterpret_cast<const uint4*>(lo);
+                    *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(0u, 0u);
+                    *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(0u, 0u);
+                }
+            }
+        }
+        if (a.hi) {   // then the entries of the tokens' experts: eight lanes per slot
+            __syncthreads();
+            for (int i = tid >> 3; i < rows * a.K; i += 32) {
+                const int m = m0 + i / a.K, j = i % a.K;
+                if (tok0 + m >= a.T) break;
+                const int k = s.rank[m][j], cb = s.col[m][j];
+                const float w = s.w[m][j];
+                for (int c = max(cb, 0) + (tid & 7); c < min(cb + k, NCH); c += 8) {
+                    float v = 0.f;
+                    for (int q = 0; q < CS; ++q) v += CS > 1 ? *cl.map_shared_rank(&s.part[m][c], q) : s.part[m][c];
+                    const float p = s.bad[c] ? NAN : w * v;
+                    const __nv_bfloat16 hi = __float2bfloat16_rn(p);
+                    const float h = __bfloat162float(hi);
+                    const int64_t at = (int64_t)(tok0 + m) * a.Rp + r0 + c;
+                    a.hi[at] = hi;
+                    a.lo[at] = __float2bfloat16_rn(fabsf(h) < INFINITY ? p - h : 0.f);
                 }
             }
         }
