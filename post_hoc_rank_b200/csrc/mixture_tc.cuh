@@ -318,22 +318,28 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
         // this CTA's rows of the tile.  Raw sums and the zeros of P first, whole rows at a time;
         // the loads of a batch of pieces (remote shared memory among them) go out together
         const int rows = kMtM / CS, m0 = rank * rows;
-        constexpr int V = NCH / 4, kBatch = 4;   // four-column pieces per row
+        constexpr int V = NCH / 4, kBatch = 2;   // four-column pieces per row
         for (int i0 = tid; i0 < rows * V; i0 += 256 * kBatch) {
             float4 v[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int q = 0; q < CS && a.raw; ++q) {
-                float4 p[kBatch];
+            for (int q0 = 0; q0 < CS && a.raw; q0 += 4) {
+                float4 p[4][kBatch];
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) {
-                    const int i = i0 + 256 * u, m = m0 + i / V, c = i % V * 4;
-                    p[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (i < rows * V && c < n && tok0 + m < a.T)
-                        p[u] = *reinterpret_cast<const float4*>(CS > 1 ? cl.map_shared_rank(&s.part[m][c], q) : &s.part[m][c]);
-                }
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int u = 0; u < kBatch; ++u) v[u].x += p[u].x, v[u].y += p[u].y, v[u].z += p[u].z, v[u].w += p[u].w;
+                    for (int u = 0; u < kBatch; ++u) {
+                        const int i = i0 + 256 * u, m = m0 + i / V, c = i % V * 4;
+                        p[q][u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (q0 + q < CS && i < rows * V && c < n && tok0 + m < a.T)
+                            p[q][u] = *reinterpret_cast<const float4*>(CS > 1 ? cl.map_shared_rank(&s.part[m][c], q0 + q)
+                                                                             : &s.part[m][c]);
+                    }
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int u = 0; u < kBatch; ++u)
+                        v[u].x += p[q][u].x, v[u].y += p[q][u].y, v[u].z += p[q][u].z, v[u].w += p[q][u].w;
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
@@ -355,8 +361,12 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
                 const int k = s.rank[m][j], cb = s.col[m][j];
                 const float w = s.w[m][j];
                 for (int c = max(cb, 0) + (tid & 7); c < min(cb + k, NCH); c += 8) {
-                    float v = 0.f;
-                    for (int q = 0; q < CS; ++q) v += CS > 1 ? *cl.map_shared_rank(&s.part[m][c], q) : s.part[m][c];
+                    float part[8], v = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        part[q] = q >= CS ? 0.f : (CS > 1 ? *cl.map_shared_rank(&s.part[m][c], q) : s.part[m][c]);
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) v += part[q];
                     const float p = s.bad[c] ? NAN : w * v;
                     const __nv_bfloat16 hi = __float2bfloat16_rn(p);
                     const float h = __bfloat162float(hi);
@@ -380,7 +390,7 @@ struct MixExpandSmem {
     unsigned char p[kMtExpandStages][2][kMtM * 128];        // hi, lo: 128 tokens x 64 rows
     unsigned char b[kMtExpandStages][4][kMtKB * 128];       // 64 rows x 256 columns, four pieces of 64 columns
     unsigned char y[4][kMtM * 128];                         // 128 tokens x 256 columns, four pieces of 64 columns
-    uint64_t full[kMtExpandStages], empty[kMtExpandStages], dfull[2], dempty[2], ybase;
+    uint64_t full[kMtExpandStages], empty[kMtExpandStages], dfull[2], dempty[2], ybase[4];
     uint32_t tmem;
 };
 constexpr int kMtExpandThreads = 320;   // warps 0-7 epilogue, 8 copies, 9 products
@@ -408,7 +418,7 @@ __global__ void __launch_bounds__(kMtExpandThreads, 1)
             mbar_init(&s.dfull[i], 1);
             mbar_init(&s.dempty[i], 8);
         }
-        mbar_init(&s.ybase, 1);
+        for (int i = 0; i < 4; ++i) mbar_init(&s.ybase[i], 1);
         fence_barrier_init();
     }
     tc::fence_before_sync();
@@ -459,68 +469,66 @@ __global__ void __launch_bounds__(kMtExpandThreads, 1)
             if (ok) tc::commit_warp(&s.dfull[j & 1]);
         }
         if (ok && mine > 0) ok = __all_sync(0xffffffffu, mbar_wait(&s.dfull[(mine - 1) & 1], (uint32_t)((mine - 1) / 2) & 1));
-    } else {   // ---- epilogue: y = base + D, by way of shared memory
+    } else {   // ---- epilogue: y = base + D by way of shared memory, 64 columns at a time in a ring of
+               // four buffers, so that bases arrive and tiles leave while others are worked on
         const int m = 32 * (warp & 3) + lane, half = warp >> 2;
-        auto load_base = [&](int j) {   // thread 0: the tile's base, once the store of the tile before has read the buffer
-            const int tile = (int)blockIdx.x + j * (int)gridDim.x;
-            mbar_arrive_expect_tx(&s.ybase, 4 * kMtM * 128);
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                tc::tma_load_2d(s.y[q], &basemap, tile % nct * kMtN + 64 * q, tile / nct * kMtM, &s.ybase);
+        const int nq = 4 * mine;   // quarters of tiles
+        auto load_base = [&](int i) {   // thread 0
+            const int tile = (int)blockIdx.x + (i >> 2) * (int)gridDim.x;
+            mbar_arrive_expect_tx(&s.ybase[i & 3], kMtM * 128);
+            tc::tma_load_2d(s.y[i & 3], &basemap, tile % nct * kMtN + 64 * (i & 3), tile / nct * kMtM, &s.ybase[i & 3]);
         };
         int loaded = 0;
-        if (tid == 0 && a.has_base && mine > 0) {
-            load_base(0);
-            loaded = 1;
-        }
-        for (int j = 0; j < mine; ++j) {
-            const int tile = (int)blockIdx.x + j * (int)gridDim.x;
-            ok = mbar_wait(&s.dfull[j & 1], (uint32_t)(j / 2) & 1);
-            if (a.has_base) ok = ok && mbar_wait(&s.ybase, (uint32_t)j & 1);
-            ok = tc::named_sync_and(1, 256, ok);   // every thread is here: the buffer holds the base, or is free
-            if (!ok) break;                        // the other warps' waits run out as well
-            tc::fence_after_sync();
+        if (tid == 0 && a.has_base)
+            for (; loaded < min(3, nq); ++loaded) load_base(loaded);
+        for (int i = 0; i < nq; ++i) {
+            const int j = i >> 2, tile = (int)blockIdx.x + j * (int)gridDim.x;
+            if ((i & 3) == 0) ok = mbar_wait(&s.dfull[j & 1], (uint32_t)(j / 2) & 1);
+            if (a.has_base) ok = ok && mbar_wait(&s.ybase[i & 3], (uint32_t)j & 1);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) {
+                tc::fence_after_sync();
 #pragma unroll
-            for (int c16 = 0; c16 < kMtN / 32; ++c16) {
-                const int c = (kMtN / 2) * half + 16 * c16;
-                float v[16];
-                tc::tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)((j & 1) * kMtN + c), v);
+                for (int c16 = 0; c16 < 2; ++c16) {
+                    const int c = 32 * half + 16 * c16;   // column of the quarter
+                    float v[16];
+                    tc::tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)((j & 1) * kMtN + 64 * (i & 3) + c), v);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int cc = c + 8 * h;
-                    uint4* p = reinterpret_cast<uint4*>(s.y[cc >> 6] + m * 128 + ((((cc >> 3) & 7) ^ (m & 7)) << 4));
-                    uint4 u = make_uint4(0, 0, 0, 0);
-                    if (a.has_base) u = *p;
-                    __nv_bfloat162* q = reinterpret_cast<__nv_bfloat162*>(&u);
+                    for (int h = 0; h < 2; ++h) {
+                        uint4* p = reinterpret_cast<uint4*>(s.y[i & 3] + m * 128 + ((((c >> 3) + h) ^ (m & 7)) << 4));
+                        uint4 u = make_uint4(0, 0, 0, 0);
+                        if (a.has_base) u = *p;
+                        __nv_bfloat162* q = reinterpret_cast<__nv_bfloat162*>(&u);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = __bfloat1622float2(q[i]);
-                        q[i] = __floats2bfloat162_rn(f.x + v[8 * h + 2 * i], f.y + v[8 * h + 2 * i + 1]);
+                        for (int x = 0; x < 4; ++x) {
+                            const float2 f = __bfloat1622float2(q[x]);
+                            q[x] = __floats2bfloat162_rn(f.x + v[8 * h + 2 * x], f.y + v[8 * h + 2 * x + 1]);
+                        }
+                        *p = u;
                     }
-                    *p = u;
                 }
+                if ((i & 3) == 3) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive1(&s.dempty[j & 1]);
+                }
+                tc::fence_proxy_async();
             }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive1(&s.dempty[j & 1]);
-            tc::fence_proxy_async();
-            tc::named_sync(1, 256);
+            ok = tc::named_sync_and(1, 256, ok);
+            if (!ok) break;   // the other warps' waits run out as well
             if (tid == 0) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    tc::tma_store_2d(&ymap, tile % nct * kMtN + 64 * q, tile / nct * kMtM, s.y[q]);
+                tc::tma_store_2d(&ymap, tile % nct * kMtN + 64 * (i & 3), tile / nct * kMtM, s.y[i & 3]);
                 tc::bulk_commit();
-                tc::bulk_wait_read0();
-                if (a.has_base && j + 1 < mine) {
-                    load_base(j + 1);
-                    loaded = j + 2;
+                tc::bulk_wait_read1();   // the store before has read its buffer, that of quarter i + 3
+                if (a.has_base && i + 3 < nq) {
+                    load_base(i + 3);
+                    loaded = i + 4;
                 }
             }
-            if (!a.has_base) tc::named_sync(1, 256);   // the store has read the buffer
         }
         if (tid == 0) {   // nothing is in flight when the CTA leaves
             tc::bulk_wait0();
-            if (loaded > 0) mbar_wait(&s.ybase, (uint32_t)(loaded - 1) & 1);
+            for (int i = max(0, loaded - 4); i < loaded; ++i) mbar_wait(&s.ybase[i & 3], (uint32_t)(i >> 2) & 1);
         }
     }
     tc::fence_before_sync();
