@@ -1330,13 +1330,16 @@ static int log2_of(int v) {
     return l;
 }
 
-// threads of a row-wise kernel: 8 columns each, whole warps
-static int w4_row_threads(int d_in) { return (int)std::min<int64_t>(256, align_up(d_in / 8, 32)); }
+// threads of a row-wise kernel over `pieces`: whole warps, as few passes and idle threads as 256 allow
+static int w4_row_threads(int pieces) {
+    const int passes = (int)cdiv(pieces, 256);
+    return (int)align_up(cdiv(pieces, passes), 32);
+}
 
 template <typename T>
 static cudaError_t launch_w4_quantize(const W4QuantArgs& a, int group, cudaStream_t s) {
     const unsigned grid = (unsigned)a.d_out;
-    const int thr = w4_row_threads(a.d_in);
+    const int thr = w4_row_threads(a.d_in / 16);
     switch (group) {
         case 32: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 32>), grid, thr, 0, s, a); break;
         case 64: LF_LAUNCH("w4_quantize", (w4_quantize_kernel<T, 64>), grid, thr, 0, s, a); break;
@@ -2522,8 +2525,8 @@ lf_status lf_w4_dequantize(const void* q, const void* scales, const void* zeros,
     W4DequantArgs a{reinterpret_cast<const uint8_t*>(q), reinterpret_cast<const __nv_bfloat16*>(scales),
                     reinterpret_cast<const uint8_t*>(zeros), d_out, d_in, (int32_t)cdiv(d_in, group), log2_of(group), W};
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)d_out;
-    const int thr = w4_row_threads(d_in);
+    const unsigned grid = (unsigned)cdiv(d_out, kW4DeqRows);
+    const int thr = w4_row_threads(d_in / 8);
     if (W_type == LF_F32) LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<float>, grid, thr, 0, s, a);
     else if (W_type == LF_BF16) LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<__nv_bfloat16>, grid, thr, 0, s, a);
     else LF_LAUNCH("w4_dequantize", w4_dequantize_kernel<__half>, grid, thr, 0, s, a);

@@ -10,6 +10,7 @@
 #include <cuda.h>   // CUtensorMap (type only)
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "apply_common.cuh"
 #include "router.cuh"
@@ -21,56 +22,90 @@ namespace lf {
 // Symmetric: s = bf16(max|w| / 7), z = 8.  With zero points: lo = min(w, 0), hi = max(w, 0),
 // s = bf16((hi - lo) / 15), z = clamp(rint(-lo / s), 0, 15).  q = clamp(rint(w / s) + z, 0, 15)
 // with the rounded s; every rint is of the exact quotient, halves to even.
-// G / 8 lanes per group, 8 weights each: one 16- or 32-byte read and one 4-byte write per
-// lane, the group's extremes by shuffles.  Bound by the read of W (a bf16 18944 x 3584
-// matrix: 136 MB in, 36 MB out, 26 us).
+// G / 16 lanes per group, 16 weights each, the group's extremes by shuffles.  The read of W
+// bounds it (a bf16 18944 x 3584 matrix: 136 MB in, 36 MB out, 26 us) if the instructions
+// stay below it: scales by a product with a constant and quotients by a product with an
+// approximate reciprocal, two columns per packed fp32 instruction, each followed by one test
+// (per 16 weights) that sends what lies next to a border the exact way.
 
-// rint(w / s) for s >= 2^-100 and |w / s| < 2^6, inv = 1 / s: w * inv is within 2^-22 |w / s| of
-// the quotient, so only a product next to a half can round the wrong way; the sign of
-// w - (q +- 1/2) s settles that exactly (one fma: the product is exact inside it).
-__device__ __forceinline__ float rint_quotient(float w, float s, float inv) {
-    const float t = w * inv;
-    float q = rintf(t);
-    if (fabsf(fabsf(t - q) - 0.5f) < 0x1p-12f) {
-        const float up = fmaf(-(q + 0.5f), s, w), dn = fmaf(-(q - 0.5f), s, w);
-        const bool odd = ((int)q & 1) != 0;
-        if (up > 0.f || (up == 0.f && odd)) q += 1.f;
-        else if (dn < 0.f || (dn == 0.f && odd)) q -= 1.f;
-    }
-    return q;
+__device__ __forceinline__ float2 fadd2(float2 a, float2 b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(d)
+        : "l"(*reinterpret_cast<const unsigned long long*>(&a)), "l"(*reinterpret_cast<const unsigned long long*>(&b)));
+    return *reinterpret_cast<const float2*>(&d);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
 }
 
-// bf16(num / den) of the exact quotient (num exact in fp64): fp32 division unless that
-// lands next to the middle of two bf16 values.
+constexpr float kRintMagic = 12582912.f;   // 1.5 2^23: adding it rounds to an integer, halves to even
+
+// rint(w / s) for s >= 2^-100 and |w / s| < 2^6 from an integer q off by at most one: the
+// residual w - q s is exact in one fma, and is compared with s / 2; halves go to even.
+__device__ __forceinline__ float rint_quotient(float w, float s, float q) {
+    const float e = fmaf(-q, s, w), a = fabsf(e), h = 0.5f * s;
+    const bool odd = (__float_as_uint(q + kRintMagic) & 1u) != 0;
+    return a > h || (a == h && odd) ? q + copysignf(1.f, e) : q;
+}
+
+// bf16((hi - lo) / den) of the exact quotient: a product with 1 / den unless that lands next
+// to the middle of two bf16 values (or near the ends of the range).
 __device__ __forceinline__ float bf16_quotient(float hi, float lo, float den) {
-    float f = (hi - lo) / den;
+    float f = (hi - lo) * (1.f / den);
     const uint32_t low = __float_as_uint(f) & 0xffffu;
     if (!(f < 1e38f) || f < 1e-37f || (low >= 0x7ff0u && low <= 0x8010u))
         f = (float)(((double)hi - (double)lo) / (double)den);
     return __bfloat162float(__float2bfloat16_rn(f));
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-    bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(p)), v);
-}
-template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float (&v)[8]) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
-    const __half2* h = reinterpret_cast<const __half2*>(&u);
+// 16 consecutive weights as fp32 pairs, with their smallest and largest value (0 included);
+// false when one is not finite.
+__device__ __forceinline__ bool load16(const float* p, float2 (&v)[8], float& lo, float& hi) {
+    float chk = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(h[i]);
-        v[2 * i] = f.x;
-        v[2 * i + 1] = f.y;
+        const float4 a = __ldg(reinterpret_cast<const float4*>(p) + i);
+        v[2 * i] = make_float2(a.x, a.y);
+        v[2 * i + 1] = make_float2(a.z, a.w);
+        lo = fminf(fminf(lo, fminf(a.x, a.y)), fminf(a.z, a.w));
+        hi = fmaxf(fmaxf(hi, fmaxf(a.x, a.y)), fmaxf(a.z, a.w));
+        chk = fmaf(a.x, 0.f, fmaf(a.y, 0.f, fmaf(a.z, 0.f, fmaf(a.w, 0.f, chk))));   // NaN once one is not finite
     }
+    return chk == 0.f;
+}
+template <typename H2>   // __nv_bfloat162 or __half2
+__device__ __forceinline__ bool load16_half(const void* p, float2 (&v)[8], float& lo, float& hi) {
+    uint4 u[2] = {__ldg(reinterpret_cast<const uint4*>(p)), __ldg(reinterpret_cast<const uint4*>(p) + 1)};
+    const H2* h = reinterpret_cast<const H2*>(u);
+    H2 mn = h[0], mx = h[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        mn = __hmin2_nan(mn, h[i]);
+        mx = __hmax2_nan(mx, h[i]);
+    }
+    float2 a, b;
+    if constexpr (sizeof(H2) == 4 && std::is_same<H2, __nv_bfloat162>::value) {
+        a = __bfloat1622float2(mn), b = __bfloat1622float2(mx);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __bfloat1622float2(h[i]);
+    } else {
+        a = __half22float2(mn), b = __half22float2(mx);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __half22float2(h[i]);
+    }
+    const float low = a.x + a.y, high = b.x + b.y;   // NaN or infinite once one is not finite (or their sum overflows)
+    lo = fminf(lo, fminf(a.x, a.y));
+    hi = fmaxf(hi, fmaxf(b.x, b.y));
+    return fabsf(low) < INFINITY && fabsf(high) < INFINITY;
+}
+__device__ __forceinline__ bool load16(const __nv_bfloat16* p, float2 (&v)[8], float& lo, float& hi) {
+    return load16_half<__nv_bfloat162>(p, v, lo, hi);
+}
+__device__ __forceinline__ bool load16(const __half* p, float2 (&v)[8], float& lo, float& hi) {
+    return load16_half<__half2>(p, v, lo, hi);
 }
 
 struct W4QuantArgs {
@@ -84,68 +119,93 @@ struct W4QuantArgs {
 // CTA per row, blockDim a multiple of 32.
 template <typename T, int G>
 __global__ void __launch_bounds__(256) w4_quantize_kernel(W4QuantArgs a) {
-    constexpr int L = G / 8;   // lanes per group
+    constexpr int L = G / 16;   // lanes per group
     const int64_t row = blockIdx.x;
     const T* src = reinterpret_cast<const T*>(a.W) + row * a.d_in;
     uint8_t* dst = a.q + row * (a.d_in >> 1);
     const int sub = threadIdx.x % L;
-    const int n8 = a.d_in >> 3;
-    const int n8r = (n8 + 31) & ~31;   // whole warps walk the row: the shuffles below see every lane
-    for (int p = threadIdx.x; p < n8r; p += blockDim.x) {
-        float v[8];
-        const bool in = p < n8;
+    const int np = a.d_in >> 4;        // pieces of 16 columns (d_in is a multiple of 32)
+    const int npr = (np + 31) & ~31;   // whole warps walk the row: the shuffles below see every lane
+    for (int p = threadIdx.x; p < npr; p += blockDim.x) {
+        float2 v[8];
+        const bool in = p < np;
+        float lo = 0.f, hi = 0.f;
         if (in) {
-            load8<T>(src + 8 * p, v);
+            if (!load16(src + 16 * p, v, lo, hi)) {   // (or, rarely, two huge values whose sum overflows)
+                bool bad = false;
+                lo = hi = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (!(fabsf(v[i].x) < INFINITY)) bad = true, v[i].x = 0.f;
+                    if (!(fabsf(v[i].y) < INFINITY)) bad = true, v[i].y = 0.f;
+                    lo = fminf(lo, fminf(v[i].x, v[i].y));
+                    hi = fmaxf(hi, fmaxf(v[i].x, v[i].y));
+                }
+                if (bad) latch_error(LF_ERR_NUMERIC);
+            }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        }
-        float lo = 0.f, hi = 0.f, chk = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            lo = fminf(lo, v[i]);
-            hi = fmaxf(hi, v[i]);
-            chk = fmaf(v[i], 0.f, chk);   // NaN once a value is not finite
-        }
-        if (chk != 0.f) {
-            latch_error(LF_ERR_NUMERIC);
-            lo = hi = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if (!(fabsf(v[i]) < INFINITY)) v[i] = 0.f;
-                lo = fminf(lo, v[i]);
-                hi = fmaxf(hi, v[i]);
-            }
+            for (int i = 0; i < 8; ++i) v[i] = make_float2(0.f, 0.f);
         }
 #pragma unroll
         for (int o = L / 2; o > 0; o >>= 1) {
             lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
             hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
         }
-        float s, z;
-        if (a.zeros) s = bf16_quotient(hi, lo, 15.f);
-        else s = bf16_quotient(fmaxf(hi, -lo), 0.f, 7.f);
-        uint32_t w;
+        const float s = a.zeros ? bf16_quotient(hi, lo, 15.f) : bf16_quotient(fmaxf(hi, -lo), 0.f, 7.f);
+        float z = 8.f;
+        uint32_t w[2];
         if (s >= 0x1p-100f) {
-            const float inv = 1.f / s;
-            z = a.zeros ? fminf(fmaxf(rint_quotient(-lo, s, inv), 0.f), 15.f) : 8.f;
-            w = 0;
+            const float inv = rcp_approx(s);
+            if (a.zeros) {
+                z = rint_quotient(-lo, s, (fmaf(-lo, inv, kRintMagic)) - kRintMagic);
+                z = fminf(fmaxf(z, 0.f), 15.f);
+            }
+            // code = rint(w / s) + z in the low bits of u = 1.5 2^23 + z + w * inv: |w / s| <= 15.1, so
+            // w * inv is within 2^-18 of the quotient; what lies that close to a half is settled exactly
+            const float2 inv2 = make_float2(inv, inv), ninv2 = make_float2(-inv, -inv);
+            const float2 up = make_float2(kRintMagic + z, kRintMagic + z), dn = make_float2(-kRintMagic - z, -kRintMagic - z);
+            float2 u[8];
+            float far = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float q = fminf(fmaxf(rint_quotient(v[i], s, inv) + z, 0.f), 15.f);
-                w |= __float_as_uint(q + 8388608.f) << (4 * i);   // 2^23 + q: the integer in the low bits
-                if (i < 7) w &= (1u << (4 * i + 4)) - 1u;
+                u[i] = ffma2(v[i], inv2, up);
+                const float2 d = ffma2(v[i], ninv2, fadd2(u[i], dn));
+                far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+            }
+            if (far > 0.5f - 0x1p-17f) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    u[i].x = rint_quotient(v[i].x, s, u[i].x + dn.x) + up.x;
+                    u[i].y = rint_quotient(v[i].y, s, u[i].y + dn.y) + up.y;
+                }
+            }
+            // codes are 0 or more (rint is odd), and 15 or less without zero points
+            if (a.zeros) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    u[i].x = fminf(u[i].x, kRintMagic + 15.f);
+                    u[i].y = fminf(u[i].y, kRintMagic + 15.f);
+                }
+            }
+            w[0] = w[1] = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t c = __float_as_uint(i & 1 ? u[i >> 1].y : u[i >> 1].x) << (4 * (i & 7));
+                w[i >> 3] = (w[i >> 3] & ~(15u << (4 * (i & 7)))) | (c & (15u << (4 * (i & 7))));
             }
         } else {   // 1 / s may overflow, and s may be 0
-            z = a.zeros ? (s > 0.f ? (float)fmin(fmax(rint(-(double)lo / (double)s), 0.0), 15.0) : 0.f) : 8.f;
-            w = 0;
-            for (int i = 0; i < 8; ++i) {
-                const double q = s > 0.f ? rint((double)v[i] / (double)s) : 0.0;
-                w |= (uint32_t)fmin(fmax(q + (double)z, 0.0), 15.0) << (4 * i);
+            if (a.zeros) z = s > 0.f ? (float)fmin(fmax(rint(-(double)lo / (double)s), 0.0), 15.0) : 0.f;
+            w[0] = w[1] = 0;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = i & 1 ? v[i >> 1].y : v[i >> 1].x;
+                const double q = s > 0.f ? rint((double)x / (double)s) : 0.0;
+                w[i >> 3] |= (uint32_t)fmin(fmax(q + (double)z, 0.0), 15.0) << (4 * (i & 7));
             }
         }
         if (in) {
-            *reinterpret_cast<uint32_t*>(dst + 4 * p) = w;
+            *reinterpret_cast<uint2*>(dst + 8 * p) = make_uint2(w[0], w[1]);
             if (sub == 0) {
                 const int64_t gi = row * a.ng + p / L;
                 a.scales[gi] = __float2bfloat16_rn(s);   // exact: s is a bf16 value
@@ -156,6 +216,7 @@ __global__ void __launch_bounds__(256) w4_quantize_kernel(W4QuantArgs a) {
 }
 
 // W = (q - z) * s, one rounding to the output type (none for fp32: 13 significant bits).
+// Bound by the write of W.
 struct W4DequantArgs {
     const uint8_t* q;
     const __nv_bfloat16* scales;
@@ -188,22 +249,31 @@ __device__ __forceinline__ void store8<__half>(__half* p, const float (&v)[8]) {
     *reinterpret_cast<uint4*>(p) = u;
 }
 
+// CTA per kW4DeqRows rows: a thread has that many reads in flight.
+constexpr int kW4DeqRows = 4;
 template <typename T>
 __global__ void __launch_bounds__(256) w4_dequantize_kernel(W4DequantArgs a) {
-    const int64_t row = blockIdx.x;   // CTA per row
-    const uint32_t* src = reinterpret_cast<const uint32_t*>(a.q + row * (a.d_in >> 1));
-    T* dst = reinterpret_cast<T*>(a.W) + row * a.d_in;
+    const int row0 = (int)blockIdx.x * kW4DeqRows;
     const int n8 = a.d_in >> 3;
-#pragma unroll 2
     for (int p = threadIdx.x; p < n8; p += blockDim.x) {
-        const int64_t gi = row * a.ng + (p >> (a.log_g - 3));
-        const uint32_t w = __ldg(src + p);
-        const float s = __bfloat162float(a.scales[gi]);
-        const float z = 8388608.f + (float)(a.zeros ? (a.zeros[gi] & 15) : 8);
-        float v[8];
+        uint32_t w[kW4DeqRows];
+        float s[kW4DeqRows], z[kW4DeqRows];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (__uint_as_float(((w >> (4 * j)) & 15u) | 0x4B000000u) - z) * s;
-        store8<T>(dst + 8 * p, v);
+        for (int r = 0; r < kW4DeqRows; ++r) {
+            const int64_t row = min(row0 + r, a.d_out - 1);
+            const int64_t gi = row * a.ng + (p >> (a.log_g - 3));
+            w[r] = __ldg(reinterpret_cast<const uint32_t*>(a.q + row * (a.d_in >> 1)) + p);
+            s[r] = __bfloat162float(a.scales[gi]);
+            z[r] = 8388608.f + (float)(a.zeros ? (a.zeros[gi] & 15) : 8);
+        }
+#pragma unroll
+        for (int r = 0; r < kW4DeqRows; ++r) {
+            if (row0 + r >= a.d_out) break;
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = (__uint_as_float(((w[r] >> (4 * j)) & 15u) | 0x4B000000u) - z[r]) * s[r];
+            store8<T>(reinterpret_cast<T*>(a.W) + (int64_t)(row0 + r) * a.d_in + 8 * p, v);
+        }
     }
 }
 
