@@ -332,6 +332,14 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// d = a b, from zero
+__device__ __forceinline__ void mma_16816_0(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 template <int NT>
 struct W4Smem {
     union {
@@ -341,39 +349,36 @@ struct W4Smem {
     uint64_t full[kW4Warps][kW4Depth];
 };
 
-// State of one warp's sums over its columns: two 16-row tiles, NT token tiles.
+// Sums of one warp over its columns: two 16-row tiles, NT token tiles; acc over all groups, part
+// and xs (sum x) over the current one.
 template <int NT>
 struct W4Acc {
     float acc[2][NT][4], part[2][NT][4], xs[NT][4];
     float sc[2][2], zf[2][2];   // scale and 128 + z of rows 16 m + 8 h + (this lane's row)
-    int grp;
 
-    __device__ __forceinline__ void clear() {
-        grp = -1;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                xs[n][i] = 0.f;
-                acc[0][n][i] = acc[1][n][i] = part[0][n][i] = part[1][n][i] = 0.f;
-            }
-    }
     // end of a group: acc += s (sum (128 + q) x - (128 + z) sum x)
     __device__ __forceinline__ void flush() {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 4; ++i)
                     acc[m][n][i] = fmaf(sc[m][i >> 1], fmaf(-zf[m][i >> 1], xs[n][i], part[m][n][i]), acc[m][n][i]);
-                    part[m][n][i] = 0.f;
-                }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) xs[n][i] = 0.f;
-        }
     }
-    // one word of each of the lane's four rows against 8 columns of x
+    // scale and zero point of every row of the tile, one row per lane in sz
+    __device__ __forceinline__ void scales(uint32_t sz, int rg) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t v = __shfl_sync(0xffffffffu, sz, 16 * m + 8 * h + rg);
+                sc[m][h] = __uint_as_float(v & 0xffff0000u);
+                zf[m][h] = 128.f + (float)(v & 15u);
+            }
+    }
+    // one word of each of the lane's four rows against 8 columns of x; a group begins with FIRST
+    template <bool FIRST>
     __device__ __forceinline__ void product(const uint32_t (&w)[2][2], const uint4 (&xv)[NT]) {
         const uint32_t one[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
         uint32_t b[NT][4];
@@ -383,7 +388,8 @@ struct W4Acc {
             b[n][1] = __byte_perm(xv[n].x, xv[n].z, 0x7632);   // (x1, x5)
             b[n][2] = __byte_perm(xv[n].y, xv[n].w, 0x5410);   // (x2, x6)
             b[n][3] = __byte_perm(xv[n].y, xv[n].w, 0x7632);   // (x3, x7)
-            mma_16816(xs[n], one, b[n][0], b[n][1]);
+            if (FIRST) mma_16816_0(xs[n], one, b[n][0], b[n][1]);
+            else mma_16816(xs[n], one, b[n][0], b[n][1]);
             mma_16816(xs[n], one, b[n][2], b[n][3]);
         }
 #pragma unroll
@@ -394,7 +400,8 @@ struct W4Acc {
                                     nibble_pair<3>(w[m][1])};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                mma_16816(part[m][n], lo, b[n][0], b[n][1]);
+                if (FIRST) mma_16816_0(part[m][n], lo, b[n][0], b[n][1]);
+                else mma_16816(part[m][n], lo, b[n][0], b[n][1]);
                 mma_16816(part[m][n], hi, b[n][2], b[n][3]);
             }
         }
@@ -438,95 +445,116 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_gemv_kernel(const __grid_
     // 8 lanes (two rows) fall on distinct banks of the swizzled stage
     const int rg = (g >> 1) | ((g & 1) << 2);
     W4Acc<NT> A;
-    A.clear();
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) A.acc[0][n][i] = A.acc[1][n][i] = 0.f;
+    // columns of the product past the last token take some token's x; they are not stored
     const __nv_bfloat16* xr[NT];
-    bool live[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        live[n] = tok0 + 8 * n + g < a.T;
-        xr[n] = P.x + (int64_t)(live[n] ? tok0 + 8 * n + g : 0) * P.x_ld;
-    }
-    // scale and zero point of row row0 + lane in group `grp` (rows past the last: any)
-    const int64_t srow = (int64_t)min(row0 + lane, P.d_out - 1) * P.ng;
-    auto enter_group = [&](int grp) {
-        if (A.grp >= 0) A.flush();
-        A.grp = grp;
-        const uint32_t s16 = __bfloat16_as_ushort(P.scales[srow + grp]);
-        const uint32_t z = P.zeros ? (P.zeros[srow + grp] & 15u) : 8u;
-        const uint32_t sz = (s16 << 16) | z;
+    for (int n = 0; n < NT; ++n) xr[n] = P.x + (int64_t)min(tok0 + 8 * n + g, a.T - 1) * P.x_ld + (WIDE ? t * 32 : t * 8);
+    // A step is what one 16-byte load per row covers: four units (WIDE; a whole group or half of
+    // one) or one unit.  Its x, scale and zero point (of row row0 + lane; rows past the last: any)
+    // are fetched a step ahead, so that their latency passes while the step before is multiplied
+    // (x of two token tiles would not fit the registers: fetched as its step begins).
+    constexpr int kUnits = WIDE ? 4 : 1, kSteps = 8 / kUnits;
+    const __nv_bfloat16* srow = P.scales + (int64_t)min(row0 + lane, P.d_out - 1) * P.ng;
+    const uint8_t* zrow = P.zeros ? P.zeros + (int64_t)min(row0 + lane, P.d_out - 1) * P.ng : nullptr;
+    const int log_u = P.log_u;
+    uint4 xn[kUnits][NT];
+    __nv_bfloat16 sn = __float2bfloat16_rn(0.f);
+    uint32_t zn = 8u;
+    auto fetch_s = [&](int u) {
+        sn = srow[u >> log_u];
+        if (zrow) zn = zrow[u >> log_u];
+    };
+    auto fetch_x = [&](int u) {
+        if (!WIDE || u + 4 <= units) {   // uniform
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t v = __shfl_sync(0xffffffffu, sz, 16 * m + 8 * h + rg);
-                A.sc[m][h] = __uint_as_float(v & 0xffff0000u);
-                A.zf[m][h] = 128.f + (float)(v & 15u);
-            }
+                for (int i = 0; i < kUnits; ++i) xn[i][n] = __ldg(reinterpret_cast<const uint4*>(xr[n] + u * 32 + 8 * i));
+        } else {   // the row ends inside the step
+            const bool in = u + t < units;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) {
+                    xn[i][n] = make_uint4(0, 0, 0, 0);
+                    if (in) xn[i][n] = __ldg(reinterpret_cast<const uint4*>(xr[n] + u * 32 + 8 * i));
+                }
+        }
     };
     bool ok = true;
+    if (n_st > 0) {
+        fetch_s(warp * 8);
+        if (NT == 1) fetch_x(warp * 8);
+    }
     for (int st = 0; st < n_st; ++st) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&full[st % kW4Depth], (uint32_t)((st / kW4Depth) & 1)));
-        if (!ok) break;   // uniform; the timeout is latched
-        const unsigned char* src = sm.ring[warp][st % kW4Depth];
+        const unsigned char* src = sm.ring[warp][st % kW4Depth] + rg * 128;
         const int u0 = (warp + kW4Warps * st) * 8;
-        if (WIDE) {
 #pragma unroll
-            for (int sb = 0; sb < 2; ++sb) {
-                if (u0 + 4 * sb >= units) break;   // uniform
-                const int grp = (u0 + 4 * sb) >> P.log_u;
-                if (grp != A.grp) enter_group(grp);
+        for (int sb = 0; sb < kSteps; ++sb) {
+            const int u = u0 + kUnits * sb;
+            if (u >= units) break;   // uniform
+            if (NT > 1) fetch_x(u);
+            uint4 xc[kUnits][NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < kUnits; ++i) xc[i][n] = xn[i][n];
+            const uint32_t sz = ((uint32_t)__bfloat16_as_ushort(sn) << 16) | (zn & 15u);
+            int un = u + kUnits;     // the next step, in this block or the warp's next
+            if (sb == kSteps - 1 || un >= units) un = u0 + 8 * kW4Warps;
+            if (un < units) {
+                fetch_s(un);
+                if (NT == 1) fetch_x(un);
+            }
+            if (sb == 0) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&full[st % kW4Depth], (uint32_t)((st / kW4Depth) & 1)));
+                if (!ok) break;   // uniform; the timeout is latched
+            }
+            if (WIDE) {
+                A.scales(sz, rg);
                 uint4 q[2][2];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        q[m][h] = *reinterpret_cast<const uint4*>(src + (16 * m + 8 * h + rg) * 128 +
-                                                                  (((4 * sb + t) ^ rg) << 4));
-                const bool in = u0 + 4 * sb + t < units;
-                const int k = (u0 + 4 * sb + t) * 32;
+                        q[m][h] = *reinterpret_cast<const uint4*>(src + (16 * m + 8 * h) * 128 + (((4 * sb + t) ^ rg) << 4));
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint4 xv[NT];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        xv[n] = make_uint4(0, 0, 0, 0);
-                        if (live[n] && in) xv[n] = __ldg(reinterpret_cast<const uint4*>(xr[n] + k + 8 * i));
-                    }
+                for (int i = 0; i < kUnits; ++i) {
                     uint32_t w[2][2];
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             w[m][h] = i == 0 ? q[m][h].x : i == 1 ? q[m][h].y : i == 2 ? q[m][h].z : q[m][h].w;
-                    A.product(w, xv);
+                    if (i == 0) A.template product<true>(w, xc[i]);
+                    else A.template product<false>(w, xc[i]);
                 }
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                if (u0 + k >= units) break;   // uniform
-                const int grp = (u0 + k) >> P.log_u;
-                if (grp != A.grp) enter_group(grp);
-                uint4 xv[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    xv[n] = make_uint4(0, 0, 0, 0);
-                    if (live[n]) xv[n] = __ldg(reinterpret_cast<const uint4*>(xr[n] + (u0 + k) * 32 + t * 8));
-                }
+                A.flush();
+            } else {
                 uint32_t w[2][2];
 #pragma unroll
                 for (int m = 0; m < 2; ++m)
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        w[m][h] = *reinterpret_cast<const uint32_t*>(src + (16 * m + 8 * h + rg) * 128 + ((k ^ rg) << 4) +
-                                                                     4 * t);
-                A.product(w, xv);
+                        w[m][h] = *reinterpret_cast<const uint32_t*>(src + (16 * m + 8 * h) * 128 + ((sb ^ rg) << 4) + 4 * t);
+                // groups of one or two units begin at every unit, at every even unit
+                if (log_u == 0 || (sb & 1) == 0) {
+                    A.scales(sz, rg);
+                    A.template product<true>(w, xc[0]);
+                } else {
+                    A.template product<false>(w, xc[0]);
+                }
+                if (log_u == 0 || (sb & 1) != 0 || u + 1 >= units) A.flush();
             }
         }
+        if (!ok) break;
         __syncwarp();   // the stage has been read
         if (lane == 0) issue(st + kW4Depth);
     }
-    if (A.grp >= 0) A.flush();
     if (!ok && lane == 0)   // no copy of this warp is in flight when the ring is reused or the CTA leaves
         for (int st = 0; st < n_st; ++st) mbar_wait(&full[st % kW4Depth], (uint32_t)((st / kW4Depth) & 1));
     if (!__syncthreads_and(ok)) return;   // the ring becomes the partial sums
