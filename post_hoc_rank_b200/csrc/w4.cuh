@@ -354,7 +354,7 @@ struct W4Smem {
 template <int NT>
 struct W4Acc {
     float acc[2][NT][4], part[2][NT][4], xs[NT][4];
-    float sc[2][2], zf[2][2];   // scale and 128 + z of rows 16 m + 8 h + (this lane's row)
+    float sc[2][2], zn[2][2];   // scale and -(128 + z) of rows 16 m + 8 h + (this lane's row)
 
     // end of a group: acc += s (sum (128 + q) x - (128 + z) sum x)
     __device__ __forceinline__ void flush() {
@@ -363,10 +363,17 @@ struct W4Acc {
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    acc[m][n][i] = fmaf(sc[m][i >> 1], fmaf(-zf[m][i >> 1], xs[n][i], part[m][n][i]), acc[m][n][i]);
+                for (int h = 0; h < 2; ++h) {
+                    const float2 d = ffma2(make_float2(zn[m][h], zn[m][h]), make_float2(xs[n][2 * h], xs[n][2 * h + 1]),
+                                           make_float2(part[m][n][2 * h], part[m][n][2 * h + 1]));
+                    const float2 r = ffma2(make_float2(sc[m][h], sc[m][h]), d,
+                                           make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]));
+                    acc[m][n][2 * h] = r.x;
+                    acc[m][n][2 * h + 1] = r.y;
+                }
     }
-    // scale and zero point of every row of the tile, one row per lane in sz
+    // scale and zero point of every row of the tile, one row per lane in sz: the scale's bf16 bits
+    // above those of -(128 + z)
     __device__ __forceinline__ void scales(uint32_t sz, int rg) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -374,7 +381,7 @@ struct W4Acc {
             for (int h = 0; h < 2; ++h) {
                 const uint32_t v = __shfl_sync(0xffffffffu, sz, 16 * m + 8 * h + rg);
                 sc[m][h] = __uint_as_float(v & 0xffff0000u);
-                zf[m][h] = 128.f + (float)(v & 15u);
+                zn[m][h] = __uint_as_float(v << 16);
             }
     }
     // one word of each of the lane's four rows against 8 columns of x; a group begins with FIRST
@@ -430,15 +437,15 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_gemv_kernel(const __grid_
         for (int i = 0; i < kW4Depth; ++i) mbar_init(&full[i], 1);
         fence_barrier_init();
     }
-    auto issue = [&](int st) {   // lane 0: block warp + 8 st of the rows into its ring slot
+    auto issue = [&](int st, int slot) {   // lane 0: block warp + 8 st of the rows into a ring slot
         if (st < n_st) {
-            uint64_t* bar = &full[st % kW4Depth];
+            uint64_t* bar = &full[slot];
             mbar_arrive_expect_tx(bar, kW4StageBytes);
-            tc::tma_load_2d(sm.ring[warp][st % kW4Depth], &maps.q[pi], (warp + kW4Warps * st) * 128, row0, bar);
+            tc::tma_load_2d(sm.ring[warp][slot], &maps.q[pi], (warp + kW4Warps * st) * 128, row0, bar);
         }
     };
     if (lane == 0)
-        for (int st = 0; st < kW4Depth; ++st) issue(st);
+        for (int st = 0; st < kW4Depth; ++st) issue(st, st);
     __syncwarp();
 
     // lane's row of a tile: rows of neighbouring g differ in bit 2, so that the 16-byte loads of
@@ -461,14 +468,14 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_gemv_kernel(const __grid_
     const __nv_bfloat16* srow = P.scales + (int64_t)min(row0 + lane, P.d_out - 1) * P.ng;
     const uint8_t* zrow = P.zeros ? P.zeros + (int64_t)min(row0 + lane, P.d_out - 1) * P.ng : nullptr;
     const int log_u = P.log_u;
-    uint4 xn[kUnits][NT];
+    uint4 xb[2][kUnits][NT];   // this step's, the next one's
     __nv_bfloat16 sn = __float2bfloat16_rn(0.f);
     uint32_t zn = 8u;
     auto fetch_s = [&](int u) {
         sn = srow[u >> log_u];
         if (zrow) zn = zrow[u >> log_u];
     };
-    auto fetch_x = [&](int u) {
+    auto fetch_x = [&](int u, uint4 (&xn)[kUnits][NT]) {
         if (!WIDE || u + 4 <= units) {   // uniform
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -488,30 +495,28 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_gemv_kernel(const __grid_
     bool ok = true;
     if (n_st > 0) {
         fetch_s(warp * 8);
-        if (NT == 1) fetch_x(warp * 8);
+        if (NT == 1) fetch_x(warp * 8, xb[0]);
     }
+    int slot = 0;
+    uint32_t parity = 0;
     for (int st = 0; st < n_st; ++st) {
-        const unsigned char* src = sm.ring[warp][st % kW4Depth] + rg * 128;
+        const unsigned char* src = sm.ring[warp][slot] + rg * 128;
         const int u0 = (warp + kW4Warps * st) * 8;
 #pragma unroll
         for (int sb = 0; sb < kSteps; ++sb) {
             const int u = u0 + kUnits * sb;
             if (u >= units) break;   // uniform
-            if (NT > 1) fetch_x(u);
-            uint4 xc[kUnits][NT];
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < kUnits; ++i) xc[i][n] = xn[i][n];
-            const uint32_t sz = ((uint32_t)__bfloat16_as_ushort(sn) << 16) | (zn & 15u);
+            uint4 (&xc)[kUnits][NT] = xb[NT > 1 ? 0 : sb & 1];
+            if (NT > 1) fetch_x(u, xc);
+            const uint32_t sz = ((uint32_t)__bfloat16_as_ushort(sn) << 16) | (zn & 15u) | 0xC300u;
             int un = u + kUnits;     // the next step, in this block or the warp's next
             if (sb == kSteps - 1 || un >= units) un = u0 + 8 * kW4Warps;
             if (un < units) {
                 fetch_s(un);
-                if (NT == 1) fetch_x(un);
+                if (NT == 1) fetch_x(un, xb[(sb + 1) & 1]);
             }
             if (sb == 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&full[st % kW4Depth], (uint32_t)((st / kW4Depth) & 1)));
+                ok = __all_sync(0xffffffffu, mbar_wait(&full[slot], parity));
                 if (!ok) break;   // uniform; the timeout is latched
             }
             if (WIDE) {
@@ -553,7 +558,11 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_gemv_kernel(const __grid_
         }
         if (!ok) break;
         __syncwarp();   // the stage has been read
-        if (lane == 0) issue(st + kW4Depth);
+        if (lane == 0) issue(st + kW4Depth, slot);
+        if (++slot == kW4Depth) {
+            slot = 0;
+            parity ^= 1;
+        }
     }
     if (!ok && lane == 0)   // no copy of this warp is in flight when the ring is reused or the CTA leaves
         for (int st = 0; st < n_st; ++st) mbar_wait(&full[st % kW4Depth], (uint32_t)((st / kW4Depth) & 1));
