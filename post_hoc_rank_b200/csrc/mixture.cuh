@@ -8,14 +8,15 @@
 #include <cooperative_groups.h>
 
 #include "apply_common.cuh"
+#include "mma.cuh"
 
 namespace lf {
 
 constexpr int kMixMaxK = 16;
 constexpr int kMixMaxRows = kMixMaxK * kMaxRank;   // directions of one token
 constexpr int kMixThreads = 512;
-constexpr int kMixSeg = 1024;      // elements of one shrink unit: four 16-byte loads per lane
-constexpr int kMixMaxSeg = 32;     // units per direction at most (longer rows use longer units)
+constexpr int kMixWarps = kMixThreads / 32;
+constexpr int kMixTile = 16;       // directions of one shrink tile (the rows of a matrix instruction)
 
 struct MixProj {
     const __nv_bfloat16* x;      // rows of x_ld
@@ -44,134 +45,133 @@ struct MixArgs {
 struct MixSmem {
     int64_t oa[kMixMaxRows], ob[kMixMaxRows];   // row offsets in the pools
     float coef[kMixMaxRows];                    // w_j s_j of the row's slot
-    float t[kMixMaxRows];                       // A' x, summed over the cluster
+    float t[kMixMaxRows];                       // forward: coef * A' x; gradient: A' x
     float u[kMixMaxRows];                       // gradient: B'^T dy
+    float tc[kMixMaxRows];                      // gradient: coef * B'^T dy
     float part[2][kMixMaxRows];                 // this CTA's share of t and u (read by the cluster)
     int32_t k[kMixMaxK], first[kMixMaxK + 1];
     int64_t soa[kMixMaxK], sob[kMixMaxK];
     float sc[kMixMaxK], w[kMixMaxK];
-    union {
-        float seg[kMixThreads / 32][8];
-        float red[kMixThreads * 8];             // expand partial sums of the row groups
-    };
+    float red[kMixThreads * 8];                 // shrink pieces; expand partial sums of the row groups
 };
 
-// part[r] = sum over [d0, d1) of v[d] * pool[off[r] + d], for r in [0, R): every warp takes
-// whole (direction) rows over this CTA's range; when there are fewer rows than warps, a
-// row's range is cut into equal pieces whose sums are added in order.  d0, d1 multiples of 8.
+// part[r] = sum over [d0, d1) of v[d] * pool[off[r] + d], for r in [0, R): tiles of 16 rows on
+// mma.sync m16n8k16 (rows = the 16-row operand, the vector in all eight columns), so that no
+// value is converted: an fp32 multiply-add per element took 2.5 instructions each, and their
+// issue bound the kernel.  Lane t of a row's four takes 16 bytes (8 elements) of each 32; the
+// order of k inside a step is that of the loads on both sides.  Warps share the tiles' ranges
+// in S pieces, added in order.  d0, d1 multiples of 8.
 __device__ __forceinline__ void mix_shrink(const __nv_bfloat16* v, const __nv_bfloat16* pool, const int64_t* off, int R,
                                            int d0, int d1, float* red, float* part) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int W = kMixThreads / 32;
-    const int len = d1 - d0;
-    int S = 1;   // pieces per row
-    while (S < kMixMaxSeg && (len + S - 1) / S > kMixSeg) ++S;
-    while (S > 1 && R * S > kMixThreads * 8) --S;
-    const int piece = ((len + S - 1) / S + 7) & ~7;
-    for (int un = warp; un < R * S; un += W) {
-        const int r = un / S, q = un - r * S;
-        const int b = d0 + q * piece, e = min(d1, b + piece);
-        const __nv_bfloat16* row = pool + off[r];
-        float acc = 0.f;
-        for (int d = b + lane * 8; d < e; d += 4 * 256) {
-            uint4 xv[4], av[4];
+    const int g = lane >> 2, t = lane & 3;
+    const int tiles = (R + kMixTile - 1) / kMixTile;
+    const int units = (d1 - d0 + 31) >> 5;
+    const int S = tiles >= kMixWarps ? 1 : (tiles > 1 ? kMixWarps / tiles : kMixWarps);   // pieces per tile
+    const int per = S == 1 ? units : (units + S - 1) / S;
+    for (int un = warp; un < tiles * S; un += kMixWarps) {
+        const int tile = S == 1 ? un : un / S, q = un - tile * S;
+        const __nv_bfloat16* ra = pool + off[min(tile * kMixTile + g, R - 1)] + d0 + 8 * t;
+        const __nv_bfloat16* rb = pool + off[min(tile * kMixTile + 8 + g, R - 1)] + d0 + 8 * t;
+        const __nv_bfloat16* rv = v + d0 + 8 * t;
+        const int e = min(units, (q + 1) * per), len = d1 - d0 - 8 * t;   // this lane's elements end at len
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int u = q * per; u < e; u += 2) {   // two steps' loads together: more do not fit 64 registers
+            uint4 a[2], b[2], x[2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (d + 256 * i < e) {
-                    av[i] = __ldg(reinterpret_cast<const uint4*>(row + d + 256 * i));
-                    xv[i] = __ldg(reinterpret_cast<const uint4*>(v + d + 256 * i));
+            for (int i = 0; i < 2; ++i) {
+                a[i] = b[i] = x[i] = make_uint4(0, 0, 0, 0);
+                if (u + i < e && (u + i) * 32 < len) {
+                    a[i] = __ldg(reinterpret_cast<const uint4*>(ra + (u + i) * 32));
+                    b[i] = __ldg(reinterpret_cast<const uint4*>(rb + (u + i) * 32));
+                    x[i] = __ldg(reinterpret_cast<const uint4*>(rv + (u + i) * 32));
                 }
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (d + 256 * i < e) {
-                    float xf[8], af[8];
-                    bf16x8_to_f32(xv[i], xf);
-                    bf16x8_to_f32(av[i], af);
-#pragma unroll
-                    for (int c = 0; c < 8; ++c) acc = fmaf(af[c], xf[c], acc);
-                }
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t lo[4] = {a[i].x, b[i].x, a[i].y, b[i].y}, hi[4] = {a[i].z, b[i].z, a[i].w, b[i].w};
+                mma_16816(acc, lo, x[i].x, x[i].y);
+                mma_16816(acc, hi, x[i].z, x[i].w);
+            }
         }
-        acc = warp_sum(acc);
-        if (lane == 0) red[un] = acc;
+        if (t == 0) {
+            red[un * kMixTile + g] = acc[0];
+            red[un * kMixTile + 8 + g] = acc[2];
+        }
     }
     __syncthreads();
     for (int r = threadIdx.x; r < R; r += kMixThreads) {
+        const int tile = r / kMixTile;
         float s = 0.f;
-        for (int q = 0; q < S; ++q) s += red[r * S + q];
+        for (int q = 0; q < S; ++q) s += red[(tile * S + q) * kMixTile + r % kMixTile];
         part[r] = s;
     }
     __syncthreads();
 }
 
-// out[c0 .. c1) = bf16(base + sum_r tc[r] pool[off[r] + c]); tc = t * coef formed here.
-// Threads cover 8-column vectors; a narrow range is covered by several groups of threads
-// that share the rows, summed through shared memory in group order.
-__device__ __forceinline__ void mix_expand(const float* t, const float* coef, const __nv_bfloat16* pool,
-                                           const int64_t* off, int R, const __nv_bfloat16* base, __nv_bfloat16* out,
-                                           int c0, int c1, float* red) {
+// out[c0 .. c1) = bf16(base + sum_r tc[r] pool[off[r] + c]).  Threads cover 8-column vectors; a
+// narrow range is covered by several groups of threads that share the rows, summed through
+// shared memory in group order.
+__device__ __forceinline__ void mix_expand(const float* tc, const __nv_bfloat16* pool, const int64_t* off, int R,
+                                           const __nv_bfloat16* base, __nv_bfloat16* out, int c0, int c1, float* red) {
     const int tid = threadIdx.x;
     const int nvec = (c1 - c0) >> 3;
     int RG = 1, nv = kMixThreads;   // row groups, threads per group
-    while (RG < 8 && nv / 2 >= nvec && 2 * RG <= R) {
+    while (RG < 16 && nv / 2 >= nvec && 2 * RG <= R) {
         RG *= 2;
         nv /= 2;
     }
     const int rg = tid / nv, vt = tid - rg * nv;
     for (int v0 = 0; v0 < nvec; v0 += nv) {
-        const int v = v0 + vt;
-        const int c = c0 + 8 * v;
-        float acc[8];
+        const bool on = v0 + vt < nvec;
+        const int c = c0 + 8 * (on ? v0 + vt : 0);
+        float2 acc[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = 0.f;
+        for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.f, 0.f);
         uint4 bv = make_uint4(0, 0, 0, 0);
-        if (v < nvec) {
-            if (rg == 0 && base) bv = *reinterpret_cast<const uint4*>(base + c);
-            int r = rg;
-            for (; r + 3 * RG < R; r += 4 * RG) {
-                uint4 pv[4];
+        if (rg == 0 && base && on) bv = *reinterpret_cast<const uint4*>(base + c);
+        if (on) {
+#pragma unroll 4
+            for (int r = rg; r < R; r += RG) {
+                const uint4 pv = __ldg(reinterpret_cast<const uint4*>(pool + off[r] + c));
+                const uint32_t w[4] = {pv.x, pv.y, pv.z, pv.w};
+                const float2 tv = make_float2(tc[r], tc[r]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) pv[i] = __ldg(reinterpret_cast<const uint4*>(pool + off[r + i * RG] + c));
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float f[8];
-                    bf16x8_to_f32(pv[i], f);
-                    const float tv = t[r + i * RG] * coef[r + i * RG];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] = fmaf(tv, f[e], acc[e]);
-                }
-            }
-            for (; r < R; r += RG) {
-                float f[8];
-                bf16x8_to_f32(__ldg(reinterpret_cast<const uint4*>(pool + off[r] + c)), f);
-                const float tv = t[r] * coef[r];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = fmaf(tv, f[e], acc[e]);
+                for (int i = 0; i < 4; ++i)
+                    acc[i] = ffma2(tv, make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)), acc[i]);
             }
         }
         if (RG > 1) {   // uniform
 #pragma unroll
-            for (int e = 0; e < 8; ++e) red[e * kMixThreads + tid] = acc[e];
+            for (int i = 0; i < 4; ++i) {
+                red[2 * i * kMixThreads + tid] = acc[i].x;
+                red[(2 * i + 1) * kMixThreads + tid] = acc[i].y;
+            }
             __syncthreads();
             if (rg == 0)
                 for (int q = 1; q < RG; ++q)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[e] += red[e * kMixThreads + q * nv + vt];
+                    for (int i = 0; i < 4; ++i) {
+                        acc[i].x += red[2 * i * kMixThreads + q * nv + vt];
+                        acc[i].y += red[(2 * i + 1) * kMixThreads + q * nv + vt];
+                    }
             __syncthreads();
         }
-        if (rg == 0 && v < nvec) {
+        if (rg == 0 && on) {
             float bf[8];
             bf16x8_to_f32(bv, bf);
             uint4 o;
-            __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&o);
+            __nv_bfloat162* y = reinterpret_cast<__nv_bfloat162*>(&o);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(bf[2 * i] + acc[2 * i], bf[2 * i + 1] + acc[2 * i + 1]);
+            for (int i = 0; i < 4; ++i) y[i] = __floats2bfloat162_rn(bf[2 * i] + acc[i].x, bf[2 * i + 1] + acc[i].y);
             *reinterpret_cast<uint4*>(out + c) = o;
         }
     }
 }
 
 __device__ __forceinline__ int mix_cut(int d, int part, int parts) {   // multiples of 8
-    return (int)((int64_t)(d >> 3) * part / parts) * 8;
+    if (parts == 1) return part * d;
+    return (int)((uint32_t)(d >> 3) * (uint32_t)part / (uint32_t)parts) * 8;   // d / 8 * 8 fits
 }
 
 // Token-parallel form.  Cluster of CS CTAs per (token, projection): each takes a piece of
@@ -236,13 +236,22 @@ __global__ void __launch_bounds__(kMixThreads, 2) mixture_token_kernel(const __g
     for (int i = tid; i < (GRAD ? 2 : 1) * R; i += kMixThreads) {
         const int h = i >= R ? 1 : 0, r = i - h * R;
         float v = 0.f;
-        for (int c = 0; c < CS; ++c) v += CS > 1 ? cl.map_shared_rank(&s.part[h][r], c)[0] : s.part[h][r];
-        (h ? s.u : s.t)[r] = v;
+        if (CS == 1) {
+            v = s.part[h][r];
+        } else {
+            for (int c = 0; c < CS; ++c) v += cl.map_shared_rank(&s.part[h][r], c)[0];
+        }
+        if (GRAD) {
+            (h ? s.u : s.t)[r] = v;
+            if (h) s.tc[r] = s.coef[r] * v;
+        } else {
+            s.t[r] = s.coef[r] * v;
+        }
     }
     __syncthreads();
     if (GRAD) {
         if (rank == 0 && a.gw) {
-            for (int j = tid >> 5; j < a.K; j += kMixThreads / 32) {
+            for (int j = tid >> 5; j < a.K; j += kMixWarps) {
                 float d = 0.f;
                 for (int r = s.first[j] + (tid & 31); r < s.first[j + 1]; r += 32) d = fmaf(s.t[r], s.u[r], d);
                 d = warp_sum(d);
@@ -253,14 +262,14 @@ __global__ void __launch_bounds__(kMixThreads, 2) mixture_token_kernel(const __g
             const __nv_bfloat16* base = P.base ? P.base + (int64_t)tok * P.out_ld : nullptr;
             __nv_bfloat16* out = P.out + (int64_t)tok * P.out_ld;
             if (R > 0 || base != out)
-                mix_expand(s.u, s.coef, P.A_pool, s.oa, R, base, out, mix_cut(P.d_in, rank, CS),
+                mix_expand(s.tc, P.A_pool, s.oa, R, base, out, mix_cut(P.d_in, rank, CS),
                            mix_cut(P.d_in, rank + 1, CS), s.red);
         }
     } else {
         const int64_t at = (int64_t)tok * P.out_ld + P.y_off;
         const __nv_bfloat16* base = P.in2 ? P.in2 + at : nullptr;
         if (R > 0 || base != P.out + at)
-            mix_expand(s.t, s.coef, P.Bt_pool, s.ob, R, base, P.out + at, mix_cut(P.d_out, rank, CS),
+            mix_expand(s.t, P.Bt_pool, s.ob, R, base, P.out + at, mix_cut(P.d_out, rank, CS),
                        mix_cut(P.d_out, rank + 1, CS), s.red);
     }
     if (CS > 1) cl.sync();   // the sums above are read by the whole cluster

@@ -10,7 +10,8 @@
 // once with whole-line loads and stays in registers; top-k is k rounds of a warp-wide
 // maximum (redux.sync on an order-preserving integer image of the key), which ends on the
 // lowest index among equals.  The floor is the row's read (a T = 16384, E = 256 fp32 batch:
-// 16.8 MB, 2.6 us); the rounds' instructions bound it.
+// 16.8 MB, 2.6 us); the instructions of the scores
+// and the rounds bound it.
 //
 // The chosen indices are exact: without a bias the key is the logit itself (both scores
 // are increasing), and a sum with a bias, formed in fp32, is trusted only where neighbours
@@ -259,25 +260,29 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_experts_kernel(Router
     if (a.bias) bmax = warp_max(bmax);
     // Rounding of a score s, relative: the hardware exponential is within 2^-22 plus that of
     // its argument (d = |l|, or m - l: 2 d 2^-24), the reciprocal and products add 2^-22, a
-    // softmax's sum EPL + 5 roundings; the sum with b is within 2^-24 of c.  s <= |c| + |b|.
-    // Two sums closer than both of their bounds may be out of order.
-    const float eps0 = 0x1p-20f + (float)(EPL + 5) * 0x1p-23f;
+    // softmax's sum EPL + 5 roundings; the sum with b is within 2^-24 of c, and the rounds below
+    // leave out its last log2(EPL) bits.  s <= |c| + |b|.  Two sums closer than both of their
+    // bounds may be out of order.
+    const float eps0 = 0x1p-20f + (float)EPL * 0x1p-22f + (a.sigmoid ? 0.f : (float)(EPL + 5) * 0x1p-23f);
     bool close = false;
     if (a.G > 1) {
         float mine = kNoScore;   // score of group `lane`
         if ((n & 31) == 0) {     // a group is whole registers: n / 32 of them
             const int per = n >> 5;
-uint32_t b1 = 0, b2 = 0;
+            uint32_t b1 = 0, b2 = 0;
+            int left = per, g = 0;
 #pragma unroll
             for (int i = 0; i < EPL; ++i) {
                 if (32 * i < E) {
                     const uint32_t kq = a.bias || a.group_top == 1 ? key[i] : (key[i] ? order_key(c[i]) : 0u);
                     b2 = max(b2, min(b1, kq));
                     b1 = max(b1, kq);
-                    if ((i + 1) % per == 0) {
-                        const float g = group_score(b1, b2, a.group_top, lane);
-                        if (lane == i / per) mine = g;
+                    if (--left == 0) {
+                        const float gs = group_score(b1, b2, a.group_top, lane);
+                        if (lane == g) mine = gs;
                         b1 = b2 = 0;
+                        left = per;
+                        ++g;
                     }
                 }
             }
@@ -316,35 +321,66 @@ uint32_t b1 = 0, b2 = 0;
             if (!((kept >> (((e * a.group_mul) >> 20) & 31)) & 1u)) key[i] = 0u;   // past E: 0 already
         }
     }
-    // K rounds (one more with a bias, to see how close the first one left out is)
     int chosen = -1;     // lane j: the j-th
     uint32_t ckey = 0;   // lane j: its key
-    uint32_t best = 0;
-    int bi = 0;
+    if (a.bias) {
+        // K + 1 rounds (one more, to see how close the first one left out is) over keys that carry
+        // the register's index in their last bits, sorted within each lane: a round is one
+        // warp-wide maximum, and its winner moves up by one.  What the cut bits decide is close
+        // anyway, and so are equal keys of two lanes.
 #pragma unroll
-    for (int i = 0; i < EPL; ++i)
-        if (key[i] > best) {
-            best = key[i];
-            bi = i;
-        }
-    const int rounds = a.bias ? a.K + 1 : a.K;
-    for (int j = 0; j < rounds; ++j) {
-        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-        if (top == 0) break;   // uniform: nothing left
-        const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(32 * bi + lane) : 0xffffffffu);
-        if (lane == j) {
-            chosen = e;
-            ckey = top;
-        }
-        if ((e & 31) == lane) {   // the winner's lane takes its next best
-            best = 0;
-            const int wi = e >> 5;
+        for (int i = 0; i < EPL; ++i)
+            if (key[i]) key[i] = (key[i] & ~(uint32_t)(EPL - 1)) | (uint32_t)(EPL - 1 - i);
 #pragma unroll
-            for (int i = 0; i < EPL; ++i) {
-                if (i == wi) key[i] = 0u;
-                if (key[i] > best) {
-                    best = key[i];
-                    bi = i;
+        for (int k = 2; k <= EPL; k *= 2)   // bitonic, descending
+#pragma unroll
+            for (int j = k / 2; j > 0; j /= 2)
+#pragma unroll
+                for (int i = 0; i < EPL; ++i)
+                    if ((i ^ j) > i) {
+                        const uint32_t hi = max(key[i], key[i ^ j]), lo = min(key[i], key[i ^ j]);
+                        key[i] = (i & k) == 0 ? hi : lo;
+                        key[i ^ j] = (i & k) == 0 ? lo : hi;
+                    }
+        for (int j = 0; j <= a.K; ++j) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, key[0]);
+            if (top == 0) break;   // uniform: nothing left
+            const uint32_t has = __ballot_sync(0xffffffffu, key[0] == top);
+            close = close || (has & (has - 1)) != 0;
+            const int from = __ffs(has) - 1;
+            if (lane == j) {
+                chosen = 32 * (EPL - 1 - (int)(top & (EPL - 1))) + from;
+                ckey = top & ~(uint32_t)(EPL - 1);
+            }
+            const bool me = lane == from;
+#pragma unroll
+            for (int i = 0; i + 1 < EPL; ++i) key[i] = me ? key[i + 1] : key[i];
+            key[EPL - 1] = me ? 0u : key[EPL - 1];
+        }
+    } else {   // exact keys: K rounds that end on the lowest index among equals
+        uint32_t best = 0;
+        int bi = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+            if (key[i] > best) {
+                best = key[i];
+                bi = i;
+            }
+        for (int j = 0; j < a.K; ++j) {
+            const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+            if (top == 0) break;   // uniform: nothing left
+            const int e = (int)__reduce_min_sync(0xffffffffu, best == top ? (uint32_t)(32 * bi + lane) : 0xffffffffu);
+            if (lane == j) chosen = e;
+            if ((e & 31) == lane) {   // the winner's lane takes its next best
+                best = 0;
+                const int wi = e >> 5;
+#pragma unroll
+                for (int i = 0; i < EPL; ++i) {
+                    if (i == wi) key[i] = 0u;
+                    if (key[i] > best) {
+                        best = key[i];
+                        bi = i;
+                    }
                 }
             }
         }
