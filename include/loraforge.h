@@ -563,14 +563,13 @@ lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids,
  * lf_w4_dequantize: W0 to fp32 (exact), bf16 or fp16 (rounded once).
  * lf_w4_projections: for up to LF_MAX_PROJECTIONS projections of one token batch, in one
  * call, y_t = bf16( bias + sum_g scale_g sum_{c in g} (q_c - zero_g) x_tc ): products
- * exact, sums in fp32, one rounding.  bias: nullable, d_out bf16.  x: T rows of x_ld, y: T
+ * exact, sums in fp32 (of (128 + q_c) x_tc and x_tc apart for up to 16 tokens), one rounding.  bias: nullable, d_out bf16.  x: T rows of x_ld, y: T
  * rows of y_ld, of which columns 0 .. d_out are written; x_ld and y_ld are multiples of 8;
  * projections may share x, but no y may overlap another y or an x.
- * Workspace: lf_w4_workspace_size(T, projs, n_proj) bytes (0: ws may be NULL).
  * Errors: LF_ERR_INVALID_ARG (null pointers, negative counts, unknown type, x_ld < d_in,
  * y_ld < d_out, reserved not 0), LF_ERR_SHAPE (d_in not a positive multiple of 32, d_out < 1, another group),
  * LF_ERR_ALIGNMENT (q, x, y, W not 16-byte aligned, scales or bias not 2-byte aligned,
- * d_out, x_ld or y_ld not a multiple of 8), LF_ERR_WORKSPACE. */
+ * d_out, x_ld or y_ld not a multiple of 8). */
 typedef struct {
     const void* x;              /* T rows of x_ld bf16 */
     void* y;                    /* T rows of y_ld bf16 */
@@ -586,9 +585,7 @@ lf_status lf_w4_quantize(const void* W, int32_t W_type, int32_t d_out, int32_t d
                          void* scales, void* zeros, lf_stream_t stream);
 lf_status lf_w4_dequantize(const void* q, const void* scales, const void* zeros, int32_t d_out, int32_t d_in,
                            int32_t group, void* W, int32_t W_type, lf_stream_t stream);
-size_t lf_w4_workspace_size(int32_t T, const lf_w4_projection* projs /*[host]*/, int32_t n_proj);
-lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs /*[host]*/, int32_t n_proj, void* ws,
-                            size_t ws_bytes, lf_stream_t stream);
+lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs /*[host]*/, int32_t n_proj, lf_stream_t stream);
 
 /* ---- Tracing (no counterpart on the pages: measurement support) --------------
  * Every kernel launch of the library is counted.  With timing enabled, each

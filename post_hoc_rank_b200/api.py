@@ -218,16 +218,18 @@ def jd_full(mods, tabs: JdTables, B_base, A_base, U, Vt, iters: int, weights=Non
 
 # ---- routed side path and 4-bit base weights ------------------------------------------------
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(device):
     """Context in which `device` is the current one (kernels launch on its current stream)."""
     if device.type != "cuda":
         raise ValueError(f"tensors must live on a CUDA device, got {device}")
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 def _expect(t, name: str, device, dtype, shape):
-    if t is not None and (t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or
-                          not t.is_contiguous()):
+    if t is not None and (t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous()):
         raise ValueError(f"{name}: contiguous {dtype} tensor of shape {tuple(shape)} on {device} expected")
 
 
@@ -266,7 +268,9 @@ def route_experts_backward(logits, router: lf.lf_router, ids, grad_weights, stre
 
 
 def _same_rows(projections, T: int):
-    if any(p.rows != T for p in projections):
+    for p in projections:
+        if p.rows == T:
+            continue
         raise ValueError(f"every projection must have {T} rows, got {[p.rows for p in projections]}")
 
 
@@ -280,6 +284,7 @@ def lora_mixture(ids, weights, n_adapters: int, projections, scale: float, adapt
     _expect(adapter_scale, "adapter_scale", dev, torch.float32, (n_adapters,))
     _same_rows(projections, ids.shape[0])
     with _on(dev):
+        projections = lf._array(lf.lf_mixture_projection, projections)
         if ws is None:
             n = lf.lf_lora_mixture_workspace_size(ids.shape[0], ids.shape[1], n_adapters, projections)
             ws = workspace(n, dev) if n else None
@@ -298,6 +303,7 @@ def lora_mixture_backward(ids, weights, n_adapters: int, grads, scale: float, ad
     _same_rows(grads, ids.shape[0])
     with _on(dev):
         gw = torch.empty(ids.shape, dtype=torch.float32, device=dev) if grad_weights else None
+        grads = lf._array(lf.lf_mixture_grad, grads)
         if ws is None:
             n = lf.lf_lora_mixture_backward_workspace_size(ids.shape[0], ids.shape[1], n_adapters, grads)
             ws = workspace(n, dev) if n else None
@@ -344,17 +350,13 @@ def w4_dequantize(w4: W4, dtype=torch.bfloat16, stream=None):
     return W
 
 
-def w4_project(projections, ws=None, stream=None):
+def w4_project(projections, stream=None):
     """y = x W0^T + bias for lf.make_w4_projection projections of one token batch
     (lf_w4_projections): all have the same number of rows of x."""
     T = projections[0].rows
     _same_rows(projections, T)
-    dev = projections[0].device
-    with _on(dev):
-        if ws is None:
-            n = lf.lf_w4_workspace_size(T, projections)
-            ws = workspace(n, dev) if n else None
-        lf.lf_w4_projections(T, projections, ws, stream)
+    with _on(projections[0].device):
+        lf.lf_w4_projections(T, projections, stream)
 
 
 def w4_linear(x, w4: W4, bias=None, out=None, stream=None):

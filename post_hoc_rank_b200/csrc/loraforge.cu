@@ -2533,17 +2533,9 @@ lf_status lf_w4_dequantize(const void* q, const void* scales, const void* zeros,
     return launch_status();
 }
 
-size_t lf_w4_workspace_size(int32_t T, const lf_w4_projection* projs, int32_t n_proj) {
-    (void)T;
-    (void)projs;
-    (void)n_proj;
-    return 0;
-}
-
 static_assert(kW4MaxProj == LF_MAX_PROJECTIONS, "projection table size");
 
-lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_proj, void* ws, size_t ws_bytes,
-                            lf_stream_t stream) {
+lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_proj, lf_stream_t stream) {
     if (T < 0 || n_proj < 1 || n_proj > LF_MAX_PROJECTIONS || !projs) return LF_ERR_INVALID_ARG;
     W4Args a{};
     a.T = T;
@@ -2585,8 +2577,6 @@ lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_
         t.ng = (int32_t)cdiv(q.d_in, q.group);
         t.log_u = log2_of(q.group / 32);
     }
-    (void)ws;
-    (void)ws_bytes;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (many) return N == 32 ? launch_w4_gemm<32>(a, maps, s) : N == 64 ? launch_w4_gemm<64>(a, maps, s) : launch_w4_gemm<128>(a, maps, s);
     W4Maps qmaps;

@@ -107,15 +107,18 @@ ROUTER_MAX_EXPERTS = 1024
 ROUTER_MAX_K = 16
 # element types of logits and weight matrices
 LF_F32, LF_BF16, LF_F16 = 0, 1, 2
-_TYPE_CODES = {"torch.float32": LF_F32, "torch.bfloat16": LF_BF16, "torch.float16": LF_F16}
+_TYPE_CODES: dict = {}
 
 
 def type_code(dtype) -> int:
     """LF_F32 / LF_BF16 / LF_F16 of a torch dtype."""
-    try:
-        return _TYPE_CODES[str(dtype)]
-    except KeyError:
-        raise ValueError(f"float32, bfloat16 or float16 expected, got {dtype}") from None
+    if not _TYPE_CODES:
+        import torch
+        _TYPE_CODES.update({torch.float32: LF_F32, torch.bfloat16: LF_BF16, torch.float16: LF_F16})
+    code = _TYPE_CODES.get(dtype)
+    if code is None:
+        raise ValueError(f"float32, bfloat16 or float16 expected, got {dtype}")
+    return code
 
 
 class LFError(RuntimeError):
@@ -194,8 +197,7 @@ def lib() -> ctypes.CDLL:
         L.lf_w4_quantize.argtypes = [_P, _I32, _I32, _I32, _I32, _P, _P, _P, _P]; L.lf_w4_quantize.restype = ctypes.c_int
         L.lf_w4_dequantize.argtypes = [_P, _P, _P, _I32, _I32, _I32, _P, _I32, _P]
         L.lf_w4_dequantize.restype = ctypes.c_int
-        L.lf_w4_workspace_size.argtypes = [_I32, _P, _I32]; L.lf_w4_workspace_size.restype = _SZ
-        L.lf_w4_projections.argtypes = [_I32, _P, _I32, _P, _SZ, _P]; L.lf_w4_projections.restype = ctypes.c_int
+        L.lf_w4_projections.argtypes = [_I32, _P, _I32, _P]; L.lf_w4_projections.restype = ctypes.c_int
         L.lf_status_string.argtypes = [ctypes.c_int]; L.lf_status_string.restype = ctypes.c_char_p
         L.lf_get_device_status.argtypes = [_P]; L.lf_get_device_status.restype = ctypes.c_int
         L.lf_profile_enable.argtypes = [ctypes.c_int]; L.lf_profile_enable.restype = None
@@ -216,7 +218,7 @@ def exported_symbols() -> list[str]:
             "lf_lora_shrink_expand_slices_routed", "lf_check_bounded_wait", "lf_pool_workspace_size",
             "lf_pool_subspace", "lf_lora_shrink_expand_projections", "lf_route_experts", "lf_route_experts_backward",
             "lf_lora_mixture_workspace_size", "lf_lora_mixture_backward_workspace_size", "lf_lora_mixture", "lf_lora_mixture_backward", "lf_w4_quantize",
-            "lf_w4_dequantize", "lf_w4_workspace_size", "lf_w4_projections"]
+            "lf_w4_dequantize", "lf_w4_projections"]
 
 # Limits of lf_lora_shrink_expand_noalloc (its scratch is a fixed array in the library).
 NOALLOC_MAX_TOKENS = 16384
@@ -226,11 +228,11 @@ NOALLOC_MAX_ADAPTERS = 4096
 def _ptr(t) -> int | None:
     if t is None:
         return None
+    if hasattr(t, "data_ptr"):
+        return t.data_ptr()
     if isinstance(t, int):
         return t
-    if isinstance(t, np.ndarray):
-        return t.ctypes.data
-    return t.data_ptr()
+    return t.ctypes.data
 
 
 def _mods_ptr(mods: np.ndarray):
@@ -241,7 +243,8 @@ def _mods_ptr(mods: np.ndarray):
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: torch.cuda.current_stream() builds a Stream object, 3 us a call
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -389,11 +392,30 @@ def lf_lora_sigma_sandwich(x, y, ids, n_adapters, Vt, Ut, sigma, diagonal, scale
     return _check(st, "lf_lora_sigma_sandwich") if check else st
 
 
-def _row_stride(t, what: str) -> int:
-    """Row stride of a 2-D bf16 tensor whose columns lie side by side."""
-    if t.dim() != 2 or str(t.dtype) != "torch.bfloat16" or (t.shape[0] > 0 and t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: a 2-D bfloat16 tensor with unit column stride expected")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+_ARRAY_TYPES: dict = {}
+
+
+def _array(kind, items):
+    """C array of the structures in `items` (itself, if it is one already)."""
+    if isinstance(items, ctypes.Array):
+        return items
+    key = (kind, len(items))
+    typ = _ARRAY_TYPES.get(key)
+    if typ is None:
+        typ = _ARRAY_TYPES[key] = kind * len(items)
+    return typ(*items)
+
+
+def _rows(t, what: str) -> tuple[int, int, int]:
+    """(rows, columns, row stride) of a 2-D bf16 tensor whose columns lie side by side."""
+    shape = t.shape
+    if len(shape) != 2 or type_code(t.dtype) != LF_BF16:
+        raise ValueError(f"{what}: a 2-D bfloat16 tensor expected")
+    n, c = shape
+    ld, step = t.stride()
+    if step != 1 and n > 0 and c > 1:
+        raise ValueError(f"{what}: a unit column stride expected")
+    return n, c, (ld if n > 1 else max(ld, c))
 
 
 def make_router(n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, top_groups: int = 1,
@@ -430,39 +452,43 @@ def lf_route_experts_backward(logits, router: lf_router, ids, grad_weights, grad
 def make_mixture_projection(x, y, sl: lf_slice, base=None) -> lf_mixture_projection:
     """lf_mixture_projection from device tensors: x T x d_in bf16, y T x y_ld bf16 (rows may be
     strided), base None (zeros) or laid out like y (y itself: in place)."""
-    y_ld = _row_stride(y, "y")
-    if base is not None and (_row_stride(base, "base") != y_ld or base.shape != y.shape):
-        raise ValueError("base must have y's shape and row stride")
-    if x.shape[0] != y.shape[0]:
+    T, d_in, x_ld = _rows(x, "x")
+    n, _, y_ld = _rows(y, "y")
+    if n != T:
         raise ValueError("x and y must have the same rows")
-    p = lf_mixture_projection(_ptr(x), _ptr(base), _ptr(y), int(x.shape[1]), 0, _row_stride(x, "x"), y_ld, sl)
-    p.rows = int(x.shape[0])
+    if base is not None and base is not y and (_rows(base, "base")[2] != y_ld or base.shape != y.shape):
+        raise ValueError("base must have y's shape and row stride")
+    p = lf_mixture_projection(x.data_ptr(), _ptr(base), y.data_ptr(), d_in, 0, x_ld, y_ld, sl)
+    p.rows = T
     return p
 
 
 def make_mixture_grad(x, dy, dx, sl: lf_slice, dx_base=None) -> lf_mixture_grad:
     """lf_mixture_grad from device tensors: x and dx T x d_in, dy T x dy_ld (bf16, rows may be
     strided); dx None = not wanted, dx_base None (zeros) or laid out like dx."""
-    dx_ld = _row_stride(dx, "dx") if dx is not None else 0
-    if dx is not None and dx.shape != x.shape:
-        raise ValueError("dx must have x's shape")
-    if dx_base is not None and (dx is None or _row_stride(dx_base, "dx_base") != dx_ld or dx_base.shape != dx.shape):
-        raise ValueError("dx_base must have dx's shape and row stride")
-    if x.shape[0] != dy.shape[0]:
+    T, d_in, x_ld = _rows(x, "x")
+    n, _, dy_ld = _rows(dy, "dy")
+    if n != T:
         raise ValueError("x and dy must have the same rows")
-    p = lf_mixture_grad(_ptr(x), _ptr(dy), _ptr(dx_base), _ptr(dx), int(x.shape[1]), 0, _row_stride(x, "x"),
-                        _row_stride(dy, "dy"), dx_ld, sl)
-    p.rows = int(x.shape[0])
+    dx_ld = 0
+    if dx is not None:
+        if dx.shape != x.shape:
+            raise ValueError("dx must have x's shape")
+        dx_ld = _rows(dx, "dx")[2]
+    if dx_base is not None and (dx is None or _rows(dx_base, "dx_base")[2] != dx_ld or dx_base.shape != dx.shape):
+        raise ValueError("dx_base must have dx's shape and row stride")
+    p = lf_mixture_grad(x.data_ptr(), dy.data_ptr(), _ptr(dx_base), _ptr(dx), d_in, 0, x_ld, dy_ld, dx_ld, sl)
+    p.rows = T
     return p
 
 
 def lf_lora_mixture_workspace_size(T: int, top_k: int, n_adapters: int, projections) -> int:
-    arr = (lf_mixture_projection * len(projections))(*projections)
+    arr = _array(lf_mixture_projection, projections)
     return lib().lf_lora_mixture_workspace_size(T, top_k, n_adapters, arr, len(projections))
 
 
 def lf_lora_mixture_backward_workspace_size(T: int, top_k: int, n_adapters: int, grads) -> int:
-    arr = (lf_mixture_grad * len(grads))(*grads)
+    arr = _array(lf_mixture_grad, grads)
     return lib().lf_lora_mixture_backward_workspace_size(T, top_k, n_adapters, arr, len(grads))
 
 
@@ -471,7 +497,7 @@ def lf_lora_mixture(ids, weights, n_adapters, projections, scale, ws=None, adapt
     """Routed side path: ids T x top_k int32, weights T x top_k fp32 or None, up to MAX_PROJECTIONS
     projections (make_mixture_projection)."""
     T, K = ids.shape
-    arr = (lf_mixture_projection * len(projections))(*projections)
+    arr = _array(lf_mixture_projection, projections)
     st = lib().lf_lora_mixture(T, K, _ptr(ids), _ptr(weights), n_adapters, arr, len(projections), float(scale),
                                _ptr(adapter_scale), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream))
     return _check(st, "lf_lora_mixture") if check else st
@@ -481,7 +507,7 @@ def lf_lora_mixture_backward(ids, weights, n_adapters, grads, scale, grad_weight
                              stream=None, check=True) -> int:
     """Gradients of lf_lora_mixture for x (per projection, make_mixture_grad) and the weights."""
     T, K = ids.shape
-    arr = (lf_mixture_grad * len(grads))(*grads)
+    arr = _array(lf_mixture_grad, grads)
     st = lib().lf_lora_mixture_backward(T, K, _ptr(ids), _ptr(weights), n_adapters, arr, len(grads), float(scale),
                                         _ptr(adapter_scale), _ptr(grad_weights), _ptr(ws),
                                         ws.numel() if ws is not None else 0, _stream(stream))
@@ -500,32 +526,44 @@ def lf_w4_quantize(W, group: int, q, scales, zeros=None, stream=None, check=True
 def lf_w4_dequantize(q, scales, zeros, group: int, W, stream=None, check=True) -> int:
     """W (d_out x d_in fp32, bf16 or fp16) = (q - zeros) * scales."""
     d_out, d_in = W.shape
+    _w4_tables(q, scales, zeros, d_out, d_in, int(group))
     st = lib().lf_w4_dequantize(_ptr(q), _ptr(scales), _ptr(zeros), d_out, d_in, int(group), _ptr(W),
                                 type_code(W.dtype), _stream(stream))
     return _check(st, "lf_w4_dequantize") if check else st
 
 
+def _w4_tables(q, scales, zeros, d_out: int, d_in: int, group: int):
+    """Checks that the tables of a 4-bit matrix have the sizes its kernels read."""
+    n = d_out * (-(-d_in // group))
+    if q.element_size() != 1 or q.numel() != d_out * (d_in // 2) or not q.is_contiguous():
+        raise ValueError("q: a contiguous d_out x d_in / 2 uint8 tensor expected")
+    if scales.numel() != n or type_code(scales.dtype) != LF_BF16 or not scales.is_contiguous():
+        raise ValueError("scales: a contiguous d_out x ceil(d_in / group) bfloat16 tensor expected")
+    if zeros is not None and (zeros.numel() != n or zeros.element_size() != 1 or not zeros.is_contiguous()):
+        raise ValueError("zeros: a contiguous d_out x ceil(d_in / group) uint8 tensor expected")
+
+
 def make_w4_projection(x, y, q, scales, group: int, zeros=None, bias=None) -> lf_w4_projection:
     """lf_w4_projection from device tensors: x T x d_in and y T x d_out bf16 (rows may be strided),
     the 4-bit weights as lf_w4_quantize lays them out, bias d_out bf16 or None."""
-    if x.shape[0] != y.shape[0] or x.shape[1] != 2 * q.shape[1] or y.shape[1] < q.shape[0]:
+    T, d_in, x_ld = _rows(x, "x")
+    n, cols, y_ld = _rows(y, "y")
+    d_out, half = q.shape
+    if n != T or d_in != 2 * half or cols < d_out:
         raise ValueError(f"shapes do not fit: x {tuple(x.shape)}, y {tuple(y.shape)}, q {tuple(q.shape)}")
-    p = lf_w4_projection(_ptr(x), _ptr(y), _ptr(q), _ptr(scales), _ptr(zeros), _ptr(bias), int(x.shape[1]),
-                         int(q.shape[0]), int(group), 0, _row_stride(x, "x"), _row_stride(y, "y"))
-    p.rows, p.device = int(x.shape[0]), x.device
+    _w4_tables(q, scales, zeros, d_out, d_in, group)
+    if bias is not None and (bias.numel() != d_out or type_code(bias.dtype) != LF_BF16 or not bias.is_contiguous()):
+        raise ValueError("bias: d_out contiguous bfloat16 values expected")
+    p = lf_w4_projection(x.data_ptr(), y.data_ptr(), q.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(bias), d_in,
+                         d_out, group, 0, x_ld, y_ld)
+    p.rows, p.device = T, x.device
     return p
 
 
-def lf_w4_workspace_size(T: int, projections) -> int:
-    arr = (lf_w4_projection * len(projections))(*projections)
-    return lib().lf_w4_workspace_size(int(T), arr, len(projections))
-
-
-def lf_w4_projections(T: int, projections, ws=None, stream=None, check=True) -> int:
+def lf_w4_projections(T: int, projections, stream=None, check=True) -> int:
     """y = x W0^T + bias for up to MAX_PROJECTIONS projections (make_w4_projection) of T tokens."""
-    arr = (lf_w4_projection * len(projections))(*projections)
-    st = lib().lf_w4_projections(int(T), arr, len(projections), _ptr(ws), ws.numel() if ws is not None else 0,
-                                 _stream(stream))
+    arr = _array(lf_w4_projection, projections)
+    st = lib().lf_w4_projections(int(T), arr, len(projections), _stream(stream))
     return _check(st, "lf_w4_projections") if check else st
 
 
