@@ -1200,7 +1200,7 @@ static lf_status launch_mix_shrink_n(const MixShrinkArgs& a, int Rmax, int cs, c
     LF_CUDA_TRY(cudaFuncSetAttribute(mixture_shrink_kernel<NCH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm));
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(cdiv(a.T, kMtM) * cs), (unsigned)cdiv(Rmax, NCH));
-    cfg.blockDim = dim3(256);
+    cfg.blockDim = dim3(kMtShrinkThreads);
     cfg.dynamicSmemBytes = sm;
     cfg.stream = s;
     cudaLaunchAttribute at[1];

@@ -175,17 +175,23 @@ struct MixShrinkSmem {
     // times scale; an expert named twice has one slot with the sum of its weights
     int16_t col[kMtM][kMixMaxK], rank[kMtM][kMixMaxK];
     float w[kMtM][kMixMaxK];
-    uint64_t full[kMtShrinkStages], empty[kMtShrinkStages], done;
+    uint64_t full[kMtShrinkStages], empty[kMtShrinkStages], dfull[2], dempty[2];
     uint32_t tmem;
     int32_t failed;
 };
+constexpr int kMtShrinkThreads = 320;   // warps 0-7 sums, 8 copies, 9 products
+// The tensor core's running fp32 sum drops what falls below it, so an error grows with the number
+// of products added up in one: after kMtSeg stages (32 of them) the sum moves to registers, whose
+// additions round (the weights' gradient of 8192 tokens of 3584 columns: 3.4e-6 off in norm with
+// sums of 1792 columns).
+constexpr int kMtSeg = 8;
 
 // xmap: T rows of d columns, box 64 x 128; amap: Rp rows of d columns, box 64 x 32; 128-byte
 // swizzle both.  Grid: clusters of CS along x (shares of d), token tiles, y = chunks of NCH rows.
-// Warp 0 issues the copies, warp 1 the products; all eight form the sums.  NCH 256: x is read
+// NCH 256: x is read
 // once for 256 rows; 128: twice the CTAs, where 256 leave most SMs idle.
 template <int NCH>
-__global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_constant__ MixShrinkArgs a,
+__global__ void __launch_bounds__(kMtShrinkThreads, 1) mixture_shrink_kernel(const __grid_constant__ MixShrinkArgs a,
                                                                 const __grid_constant__ CUtensorMap xmap,
                                                                 const __grid_constant__ CUtensorMap amap) {
     namespace cg = cooperative_groups;
@@ -202,13 +208,16 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int steps = (a.d + kMtKB - 1) / kMtKB;
     const int k0 = (int)((int64_t)steps * rank / CS), nk = (int)((int64_t)steps * (rank + 1) / CS) - k0;
-    if (warp == 0) tc::tmem_alloc(&s.tmem, NCH);
+    if (warp == 0) tc::tmem_alloc(&s.tmem, 2 * NCH);
     if (tid == 0) {
         for (int i = 0; i < kMtShrinkStages; ++i) {
             mbar_init(&s.full[i], 1);
             mbar_init(&s.empty[i], 1);
         }
-        mbar_init(&s.done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s.dfull[i], 1);
+            mbar_init(&s.dempty[i], 8);
+        }
         s.failed = 0;
         fence_barrier_init();
     }
@@ -221,7 +230,7 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
     tc::fence_after_sync();
     const uint32_t tmem = s.tmem;
     bool ok = true;
-    if (warp >= 4) {   // a thread per token: its slots, while the products run
+    if (warp >= 4 && warp < 8) {   // a thread per token: its slots, while the products run
         const int m = tid - 128, t = tok0 + m;
         const bool lead = a.report && r0 == 0 && rank == 0;
         if ((a.hi || lead) && t < a.T) {
@@ -257,7 +266,11 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
             }
         }
     }
-    if (warp == 0) {
+    const int nseg = (nk + kMtSeg - 1) / kMtSeg;
+    float acc[NCH / 2];   // columns NCH / 2 * (warp / 4) .. of row 32 (warp % 4) + lane
+#pragma unroll
+    for (int i = 0; i < NCH / 2; ++i) acc[i] = 0.f;
+    if (warp == 8) {
         if (lane == 0) {
             int i = 0;
             for (; i < nk; ++i) {
@@ -273,44 +286,59 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
             for (int j = max(0, i - kMtShrinkStages); j < i; ++j)
                 ok = mbar_wait(&s.full[j % kMtShrinkStages], (uint32_t)(j / kMtShrinkStages) & 1) && ok;
         }
-    } else if (warp == 1) {
+    } else if (warp == 9) {
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         const uint32_t idesc = tc::idesc_bf16(kMtM, n, 0, 0);
         const uint64_t xd0 = tc::smem_desc_sw128(s.x[0]), ad0 = tc::smem_desc_sw128(s.a[0]);
         for (int i = 0; i < nk; ++i) {
-            const int st = i % kMtShrinkStages;
-            ok = __all_sync(0xffffffffu, mbar_wait(&s.full[st], (uint32_t)(i / kMtShrinkStages) & 1));
+            const int st = i % kMtShrinkStages, g = i / kMtSeg;
+            ok = mbar_wait(&s.full[st], (uint32_t)(i / kMtShrinkStages) & 1);
+            if (i % kMtSeg == 0 && g >= 2) ok = ok && mbar_wait(&s.dempty[g & 1], (uint32_t)(g / 2 - 1) & 1);
+            ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t xd = xd0 + (uint64_t)(st * (kMtM * 128 / 16)), ad = ad0 + (uint64_t)(st * (NCH * 128 / 16));
+            const uint32_t d = tm + (uint32_t)((g & 1) * NCH);
 #pragma unroll
-            for (int k = 0; k < kMtKB / 16; ++k) tc::mma_bf16_warp(tm, xd + 2 * k, ad + 2 * k, idesc, i > 0 || k > 0);
+            for (int k = 0; k < kMtKB / 16; ++k) tc::mma_bf16_warp(d, xd + 2 * k, ad + 2 * k, idesc, i % kMtSeg > 0 || k > 0);
             tc::commit_warp(&s.empty[st]);
+            if (i % kMtSeg == kMtSeg - 1 || i == nk - 1) tc::commit_warp(&s.dfull[g & 1]);
         }
-        if (ok) {
-            tc::commit_warp(&s.done);
-            ok = __all_sync(0xffffffffu, mbar_wait(&s.done, 0));
+        if (ok && nseg > 0) ok = __all_sync(0xffffffffu, mbar_wait(&s.dfull[(nseg - 1) & 1], (uint32_t)((nseg - 1) / 2) & 1));
+    } else {
+        const int c0 = (warp >> 2) * (NCH / 2);
+        for (int g = 0; g < nseg; ++g) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&s.dfull[g & 1], (uint32_t)(g / 2) & 1));
+            if (!ok) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int c = 0; c < NCH / 2; c += 16) {
+                if (c0 + c < n) {   // uniform
+                    float v[16];
+                    tc::tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)((g & 1) * NCH + c0 + c), v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) acc[c + i] += v[i];
+                }
+            }
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive1(&s.dempty[g & 1]);
         }
     }
     if (!ok) s.failed = 1;
     tc::fence_before_sync();
     __syncthreads();   // all products complete, all copies landed: the stages become the partial sums
     tc::fence_after_sync();
-    {
+    if (warp < 8) {
         const int m = 32 * (warp & 3) + lane, c0 = (warp >> 2) * (NCH / 2);
-        for (int c = c0; c < min(c0 + NCH / 2, n); c += 16) {
-            float v[16];
-            tc::tmem_ld16(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)c, v);
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(&s.part[m][c + i]) =
-                    nk > 0 ? make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
+        for (int c = 0; c < NCH / 2; c += 4)
+            if (c0 + c < n) *reinterpret_cast<float4*>(&s.part[m][c0 + c]) = make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]);
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 0) tc::tmem_dealloc(tmem, NCH);
+    if (warp == 0) tc::tmem_dealloc(tmem, 2 * NCH);
     if (CS > 1) cl.sync();
     bool all_ok = s.failed == 0;
     for (int c = 0; c < CS && CS > 1; ++c) all_ok = all_ok && *cl.map_shared_rank(&s.failed, c) == 0;
@@ -319,7 +347,7 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
         // the loads of a batch of pieces (remote shared memory among them) go out together
         const int rows = kMtM / CS, m0 = rank * rows;
         constexpr int V = NCH / 4, kBatch = 2;   // four-column pieces per row
-        for (int i0 = tid; i0 < rows * V; i0 += 256 * kBatch) {
+        for (int i0 = tid; i0 < rows * V; i0 += kMtShrinkThreads * kBatch) {
             float4 v[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -329,7 +357,7 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
                 for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int u = 0; u < kBatch; ++u) {
-                        const int i = i0 + 256 * u, m = m0 + i / V, c = i % V * 4;
+                        const int i = i0 + kMtShrinkThreads * u, m = m0 + i / V, c = i % V * 4;
                         p[q][u] = make_float4(0.f, 0.f, 0.f, 0.f);
                         if (q0 + q < CS && i < rows * V && c < n && tok0 + m < a.T)
                             p[q][u] = *reinterpret_cast<const float4*>(CS > 1 ? cl.map_shared_rank(&s.part[m][c], q0 + q)
@@ -343,7 +371,7 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
-                const int i = i0 + 256 * u, m = m0 + i / V, c = i % V * 4;
+                const int i = i0 + kMtShrinkThreads * u, m = m0 + i / V, c = i % V * 4;
                 if (i >= rows * V || r0 + c >= a.Rp || tok0 + m >= a.T) continue;
                 const int64_t at = (int64_t)(tok0 + m) * a.Rp + r0 + c;
                 if (a.raw) *reinterpret_cast<float4*>(a.raw + at) = v[u];
@@ -355,7 +383,7 @@ __global__ void __launch_bounds__(256, 1) mixture_shrink_kernel(const __grid_con
         }
         if (a.hi) {   // then the entries of the tokens' experts: eight lanes per slot
             __syncthreads();
-            for (int i = tid >> 3; i < rows * a.K; i += 32) {
+            for (int i = tid >> 3; i < rows * a.K; i += kMtShrinkThreads / 8) {
                 const int m = m0 + i / a.K, j = i % a.K;
                 if (tok0 + m >= a.T) break;
                 const int k = s.rank[m][j], cb = s.col[m][j];
