@@ -221,10 +221,14 @@ def jd_full(mods, tabs: JdTables, B_base, A_base, U, Vt, iters: int, weights=Non
 _HERE = contextlib.nullcontext()
 
 
-def _on(device):
-    """Context in which `device` is the current one (kernels launch on its current stream)."""
+def _on(device, stream=None):
+    """Context in which `device` and `stream` (a torch stream or a raw handle; None = the device's
+    current one) are the current ones: what is allocated inside belongs to the stream that the
+    kernels run on, so its memory is not handed out again while they use it."""
     if device.type != "cuda":
         raise ValueError(f"tensors must live on a CUDA device, got {device}")
+    if stream is not None:
+        return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
     return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
@@ -248,10 +252,10 @@ def route_experts(logits, router: lf.lf_router, bias=None, counts=None, stream=N
     T, dev = logits.shape[0], logits.device
     _expect(bias, "bias", dev, torch.float32, (router.n_experts,))
     _expect(counts, "counts", dev, torch.int32, (router.n_experts,))
-    with _on(dev):
+    with _on(dev, stream):
         ids = torch.empty((T, router.top_k), dtype=torch.int32, device=dev)
         weights = torch.empty((T, router.top_k), dtype=torch.float32, device=dev)
-        lf.lf_route_experts(logits, router, bias, ids, weights, counts, stream)
+        lf.lf_route_experts(logits, router, bias, ids, weights, counts)
     return ids, weights
 
 
@@ -261,9 +265,9 @@ def route_experts_backward(logits, router: lf.lf_router, ids, grad_weights, stre
     T, dev = logits.shape[0], logits.device
     _expect(ids, "ids", dev, torch.int32, (T, router.top_k))
     _expect(grad_weights, "grad_weights", dev, torch.float32, (T, router.top_k))
-    with _on(dev):
+    with _on(dev, stream):
         grad = torch.empty((T, router.n_experts), dtype=logits.dtype, device=dev)
-        lf.lf_route_experts_backward(logits, router, ids, grad_weights, grad, stream)
+        lf.lf_route_experts_backward(logits, router, ids, grad_weights, grad)
     return grad
 
 
@@ -283,12 +287,12 @@ def lora_mixture(ids, weights, n_adapters: int, projections, scale: float, adapt
     _expect(weights, "weights", dev, torch.float32, ids.shape)
     _expect(adapter_scale, "adapter_scale", dev, torch.float32, (n_adapters,))
     _same_rows(projections, ids.shape[0])
-    with _on(dev):
+    with _on(dev, stream):
         projections = lf._array(lf.lf_mixture_projection, projections)
         if ws is None:
             n = lf.lf_lora_mixture_workspace_size(ids.shape[0], ids.shape[1], n_adapters, projections)
             ws = workspace(n, dev) if n else None
-        lf.lf_lora_mixture(ids, weights, n_adapters, projections, scale, ws, adapter_scale, stream)
+        lf.lf_lora_mixture(ids, weights, n_adapters, projections, scale, ws, adapter_scale)
 
 
 def lora_mixture_backward(ids, weights, n_adapters: int, grads, scale: float, adapter_scale=None, grad_weights=True,
@@ -301,13 +305,13 @@ def lora_mixture_backward(ids, weights, n_adapters: int, grads, scale: float, ad
     _expect(weights, "weights", dev, torch.float32, ids.shape)
     _expect(adapter_scale, "adapter_scale", dev, torch.float32, (n_adapters,))
     _same_rows(grads, ids.shape[0])
-    with _on(dev):
+    with _on(dev, stream):
         gw = torch.empty(ids.shape, dtype=torch.float32, device=dev) if grad_weights else None
         grads = lf._array(lf.lf_mixture_grad, grads)
         if ws is None:
             n = lf.lf_lora_mixture_backward_workspace_size(ids.shape[0], ids.shape[1], n_adapters, grads)
             ws = workspace(n, dev) if n else None
-        lf.lf_lora_mixture_backward(ids, weights, n_adapters, grads, scale, gw, ws, adapter_scale, stream)
+        lf.lf_lora_mixture_backward(ids, weights, n_adapters, grads, scale, gw, ws, adapter_scale)
     return gw
 
 
@@ -333,20 +337,20 @@ def w4_quantize(W, group: int = 128, zero_points: bool = False, stream=None) -> 
         raise ValueError(f"group must be 32, 64, 128 or 256, got {group}")
     d_out, d_in = W.shape
     dev, ng = W.device, (d_in + group - 1) // group
-    with _on(dev):
+    with _on(dev, stream):
         out = W4(torch.empty((d_out, d_in // 2), dtype=torch.uint8, device=dev),
                  torch.empty((d_out, ng), dtype=torch.bfloat16, device=dev),
                  torch.empty((d_out, ng), dtype=torch.uint8, device=dev) if zero_points else None, group)
-        lf.lf_w4_quantize(W, group, out.q, out.scales, out.zeros, stream)
+        lf.lf_w4_quantize(W, group, out.q, out.scales, out.zeros)
     return out
 
 
 def w4_dequantize(w4: W4, dtype=torch.bfloat16, stream=None):
     """The matrix a W4 stands for (lf_w4_dequantize), fp32 (exact), bf16 or fp16."""
     dev = w4.q.device
-    with _on(dev):
+    with _on(dev, stream):
         W = torch.empty(w4.shape, dtype=dtype, device=dev)
-        lf.lf_w4_dequantize(w4.q, w4.scales, w4.zeros, w4.group, W, stream)
+        lf.lf_w4_dequantize(w4.q, w4.scales, w4.zeros, w4.group, W)
     return W
 
 
@@ -355,17 +359,17 @@ def w4_project(projections, stream=None):
     (lf_w4_projections): all have the same number of rows of x."""
     T = projections[0].rows
     _same_rows(projections, T)
-    with _on(projections[0].device):
-        lf.lf_w4_projections(T, projections, stream)
+    with _on(projections[0].device, stream):
+        lf.lf_w4_projections(T, projections)
 
 
 def w4_linear(x, w4: W4, bias=None, out=None, stream=None):
     """x (T x d_in bf16) times a 4-bit matrix: T x d_out bf16 (lf_w4_projections, one projection)."""
     if x.shape[1] != w4.shape[1]:
         raise ValueError(f"x has {x.shape[1]} columns, the matrix {w4.shape[1]}")
-    with _on(x.device):
+    with _on(x.device, stream):
         y = out if out is not None else torch.empty((x.shape[0], w4.shape[0]), dtype=torch.bfloat16, device=x.device)
-        w4_project([lf.make_w4_projection(x, y, w4.q, w4.scales, w4.group, w4.zeros, bias)], stream=stream)
+        w4_project([lf.make_w4_projection(x, y, w4.q, w4.scales, w4.group, w4.zeros, bias)])
     return y
 
 

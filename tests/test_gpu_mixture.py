@@ -266,6 +266,17 @@ def test_same_results_from_run_to_run_and_captured(K, d_in, d_out):
         call()
     torch.cuda.current_stream().wait_stream(st)
     assert all(torch.equal(a, c) for a, c in zip(first, (y, dx, gw)))
+    # the workspace of a call on a named stream belongs to that stream
+    st.wait_stream(torch.cuda.current_stream())
+    for t in (y, dx):
+        t.zero_()
+    st.wait_stream(torch.cuda.current_stream())
+    api.lora_mixture(D["ids"], D["w"], 16, [lf.make_mixture_projection(D["x"], y, sl, base=D["base"])], 1.0, stream=st)
+    g2 = api.lora_mixture_backward(D["ids"], D["w"], 16, [lf.make_mixture_grad(D["x"], D["dy"], dx, sl)], 1.0,
+                                   stream=st.cuda_stream)
+    junk = [torch.full((1 << 22,), 7.0, device="cuda") for _ in range(4)]
+    torch.cuda.current_stream().wait_stream(st)
+    assert all(torch.equal(a, c) for a, c in zip(first, (y, dx, g2))) and len(junk) == 4
     gr = torch.cuda.CUDAGraph()
     with torch.cuda.graph(gr):
         call()

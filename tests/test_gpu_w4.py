@@ -165,6 +165,10 @@ def test_captured_and_on_another_stream():
             got = api.w4_linear(x, w4)
         torch.cuda.current_stream().wait_stream(st)
         assert torch.equal(got, want)
+        for arg in (st, st.cuda_stream):          # named, as a stream and as a raw handle
+            got = api.w4_linear(x, w4, stream=arg)
+            torch.cuda.current_stream().wait_stream(st)
+            assert torch.equal(got, want)
         out = torch.zeros_like(want)
         gr = torch.cuda.CUDAGraph()
         with torch.cuda.graph(gr):
