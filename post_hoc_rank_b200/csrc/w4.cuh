@@ -580,8 +580,8 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_gemv_kernel(const __grid_
 // 32 KB written and 32 KB read against 512 cycles of products at N = 128).  Blocks of 256
 // columns: one code stage, four x boxes, one A buffer.
 //   warps 0-7, unpack: two warpgroups take the blocks in turn; codes by TMA (boxes of 128 rows
-//     x 128 bytes), exact q - z, tcgen05.st (11 integer instructions per 8 weights, 704 cycles
-//     of an SM per block: about the rate at which HBM delivers the codes);
+//     x 128 bytes), exact q - z, tcgen05.st (9 integer instructions per 8 weights, 576 cycles of an
+//     SM per block against 712 in which HBM delivers its codes);
 //   warps 8-15, sums: each group's product leaves tensor memory and is added to fp32 registers
 //     times the row's scale (A stays exact, and a group's scale multiplies once, in fp32);
 //     two product buffers, so that the next group runs meanwhile;
@@ -619,11 +619,11 @@ struct W4mSmem {
 
 // 8 columns (one word) as four bf16 pairs of q - z in column order
 __device__ __forceinline__ void unpack_word(uint32_t w, __nv_bfloat162 z, uint32_t* out) {
-    const uint32_t even = w & 0x0F0F0F0Fu, odd = (w >> 4) & 0x0F0F0F0Fu;
+    const uint32_t odd = w >> 4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t p = __byte_perm(even, odd, (uint32_t)(i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12)));
-        p = (p & 0x00FF00FFu) | 0x43004300u;   // 128 + q
+    for (int i = 0; i < 4; ++i) {   // byte i of both, their low nibbles
+        uint32_t p = __byte_perm(w, odd, (uint32_t)(i | (i << 4) | ((4 + i) << 8) | ((4 + i) << 12)));
+        p = (p & 0x000F000Fu) | 0x43004300u;   // 128 + q
         const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&p), z);
         out[i] = *reinterpret_cast<const uint32_t*>(&d);
     }
@@ -764,26 +764,31 @@ __global__ void __launch_bounds__(kW4mThreads, 1) w4_gemm_kernel(const __grid_co
         const __nv_bfloat16* srow = P.scales + grow;
         const int g0 = b0 << log_d;
         const uint32_t at = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (uint32_t)(half * NH);
-        float acc[NH];
+        float2 acc[NH / 2];
 #pragma unroll
-        for (int i = 0; i < NH; ++i) acc[i] = 0.f;
-        float next = nd > 0 ? __bfloat162float(srow[min(g0, P.ng - 1)]) : 0.f;
+        for (int i = 0; i < NH / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+        const int last = P.ng - 1;
+        __nv_bfloat16 next = srow[min(g0, last)];   // kept as loaded: a conversion would wait for it
         for (int d = 0; d < nd && ok; ++d) {
-            const float sc = next;
-            next = __bfloat162float(srow[min(g0 + d + 1, P.ng - 1)]);   // arrives while this one is waited for
+            const __nv_bfloat16 cur = next;
+            next = srow[min(g0 + d + 1, last)];     // arrives while this one is waited for
             ok = __all_sync(0xffffffffu, mbar_wait(&s.dfull[d & 1], (uint32_t)(d >> 1) & 1));
             if (!ok) break;
             tc::fence_after_sync();
+            const float2 sc = make_float2(__bfloat162float(cur), __bfloat162float(cur));
 #pragma unroll
             for (int c = 0; c < NH / 16; ++c) {
                 float v[16];
                 tc::tmem_ld16(at + (uint32_t)((d & 1) * N + 16 * c), v);
+                if (c == NH / 16 - 1) {   // all read: the buffer is free for the group after next
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive1(&s.dempty[d & 1]);
+                }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) acc[16 * c + i] = fmaf(sc, v[i], acc[16 * c + i]);
+                for (int i = 0; i < 8; ++i)
+                    acc[8 * c + i] = ffma2(sc, make_float2(v[2 * i], v[2 * i + 1]), acc[8 * c + i]);
             }
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive1(&s.dempty[d & 1]);
         }
         if (ok && CS == 1) {
             const int t0 = tok0 + half * NH;
@@ -791,10 +796,11 @@ __global__ void __launch_bounds__(kW4mThreads, 1) w4_gemm_kernel(const __grid_co
 #pragma unroll
             for (int i = 0; i < NH; ++i)
                 if (row < P.d_out && t0 + i < a.T)
-                    P.y[(int64_t)(t0 + i) * P.y_ld + row] = __float2bfloat16_rn(acc[i] + bias);
+                    P.y[(int64_t)(t0 + i) * P.y_ld + row] = __float2bfloat16_rn((i & 1 ? acc[i / 2].y : acc[i / 2].x) + bias);
         } else if (ok) {   // the last product has read the last stage: the stages become this CTA's sums
 #pragma unroll
-            for (int i = 0; i < NH; ++i) s.part[half * NH + i][32 * (warp & 3) + lane] = acc[i];
+            for (int i = 0; i < NH; ++i)
+                s.part[half * NH + i][32 * (warp & 3) + lane] = i & 1 ? acc[i / 2].y : acc[i / 2].x;
         }
     } else if (warp == 16) {   // ---- TMA of the codes
         if (lane == 0) {
