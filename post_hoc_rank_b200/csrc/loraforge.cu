@@ -1311,6 +1311,11 @@ static lf_status mix_run(MixArgs& A, float* gw, void* ws, cudaStream_t s) {
         if (st != LF_OK) return st;
     }
     if (B.n_proj == 0) return LF_OK;
+    for (int p = 0; p < B.n_proj; ++p) B.p[p].slot = p;
+    // the most work per token first, so that the long CTAs start in the first waves
+    std::stable_sort(B.p, B.p + B.n_proj, [](const MixProj& u, const MixProj& v) {
+        return (int64_t)u.d_in + u.d_out > (int64_t)v.d_in + v.d_out;
+    });
     B.gw = gw;
     return launch_mixture_token<GRAD>(B, s);
 }

@@ -14,7 +14,7 @@ namespace lf {
 
 constexpr int kMixMaxK = 16;
 constexpr int kMixMaxRows = kMixMaxK * kMaxRank;   // directions of one token
-constexpr int kMixThreads = 512;
+constexpr int kMixThreads = 256;
 constexpr int kMixWarps = kMixThreads / 32;
 constexpr int kMixTile = 16;       // directions of one shrink tile (the rows of a matrix instruction)
 
@@ -24,7 +24,8 @@ struct MixProj {
     const __nv_bfloat16* base;   // gradient: dx_base (nullable: zeros)
     __nv_bfloat16* out;          // forward: y; gradient: dx (nullable)
     int64_t x_ld, dy_ld, out_ld, y_off;
-    int32_t d_in, d_out, max_rank, pad;
+    int32_t d_in, d_out, max_rank;
+    int32_t slot;                // gradient: which partial weight gradient is the projection's
     const int32_t* ranks;
     const int64_t* off_A;
     const int64_t* off_Bt;
@@ -76,10 +77,10 @@ __device__ __forceinline__ void mix_shrink(const __nv_bfloat16* v, const __nv_bf
         const __nv_bfloat16* rv = v + d0 + 8 * t;
         const int e = min(units, (q + 1) * per), len = d1 - d0 - 8 * t;   // this lane's elements end at len
         float acc[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int u = q * per; u < e; u += 2) {   // two steps' loads together: more do not fit 64 registers
-            uint4 a[2], b[2], x[2];
+        for (int u = q * per; u < e; u += 4) {
+            uint4 a[4], b[4], x[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 a[i] = b[i] = x[i] = make_uint4(0, 0, 0, 0);
                 if (u + i < e && (u + i) * 32 < len) {
                     a[i] = __ldg(reinterpret_cast<const uint4*>(ra + (u + i) * 32));
@@ -88,7 +89,7 @@ __device__ __forceinline__ void mix_shrink(const __nv_bfloat16* v, const __nv_bf
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
                 const uint32_t lo[4] = {a[i].x, b[i].x, a[i].y, b[i].y}, hi[4] = {a[i].z, b[i].z, a[i].w, b[i].w};
                 mma_16816(acc, lo, x[i].x, x[i].y);
                 mma_16816(acc, hi, x[i].z, x[i].w);
@@ -131,7 +132,7 @@ __device__ __forceinline__ void mix_expand(const float* tc, const __nv_bfloat16*
         uint4 bv = make_uint4(0, 0, 0, 0);
         if (rg == 0 && base && on) bv = *reinterpret_cast<const uint4*>(base + c);
         if (on) {
-#pragma unroll 4
+#pragma unroll 8
             for (int r = rg; r < R; r += RG) {
                 const uint4 pv = __ldg(reinterpret_cast<const uint4*>(pool + off[r] + c));
                 const uint32_t w[4] = {pv.x, pv.y, pv.z, pv.w};
@@ -180,7 +181,7 @@ __device__ __forceinline__ int mix_cut(int d, int part, int parts) {   // multip
 // shrinks, so that one token of one projection still spreads over 8 SMs; large batches use
 // single CTAs.
 template <bool GRAD>
-__global__ void __launch_bounds__(kMixThreads, 2) mixture_token_kernel(const __grid_constant__ MixArgs a) {
+__global__ void __launch_bounds__(kMixThreads, 3) mixture_token_kernel(const __grid_constant__ MixArgs a) {
     namespace cg = cooperative_groups;
     extern __shared__ __align__(16) unsigned char mix_raw[];
     MixSmem& s = *reinterpret_cast<MixSmem*>(mix_raw);
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(kMixThreads, 2) mixture_token_kernel(const __g
                 float d = 0.f;
                 for (int r = s.first[j] + (tid & 31); r < s.first[j + 1]; r += 32) d = fmaf(s.t[r], s.u[r], d);
                 d = warp_sum(d);
-                if ((tid & 31) == 0) a.gw[((int64_t)pi * a.T + tok) * a.K + j] = s.sc[j] * d;
+                if ((tid & 31) == 0) a.gw[((int64_t)P.slot * a.T + tok) * a.K + j] = s.sc[j] * d;
             }
         }
         if (P.out) {
