@@ -506,7 +506,7 @@ lf_status lf_route_experts_backward(int32_t T, const lf_router* router /*[host]*
  *   dx_t = bf16( dx_base_t + sum_j w_tj s_j A'^T (B'^T dy_t) )   (dx NULL = not wanted;
  *          dx_base NULL = zeros, may be dx itself)
  *   grad_weights[t][j] = sum over the call's projections of s_j <B'^T dy_t, A'_{e_tj} x_t>
- *          (fp32, projections in order; slots of -1 get 0; NULL = not wanted).
+ *          (fp32, in a fixed order; slots of -1 get 0; NULL = not wanted).
  * A long batch over a small pool (few stacked rows, n_adapters * max_rank; max_rank 0 counts
  * as 64) runs on the tensor cores as two dense products over the whole pool, with the
  * intermediates carried as two bf16 values (16 significant bits); other batches token by

@@ -76,7 +76,9 @@ __device__ __forceinline__ void mix_shrink(const __nv_bfloat16* v, const __nv_bf
         const __nv_bfloat16* rb = pool + off[min(tile * kMixTile + 8 + g, R - 1)] + d0 + 8 * t;
         const __nv_bfloat16* rv = v + d0 + 8 * t;
         const int e = min(units, (q + 1) * per), len = d1 - d0 - 8 * t;   // this lane's elements end at len
-        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+        // the tensor core's running sum drops what falls below it, so four units are summed there
+        // and added in registers, whose additions round
+        float s0 = 0.f, s1 = 0.f;
         for (int u = q * per; u < e; u += 4) {
             uint4 a[4], b[4], x[4];
 #pragma unroll
@@ -88,16 +90,20 @@ __device__ __forceinline__ void mix_shrink(const __nv_bfloat16* v, const __nv_bf
                     x[i] = __ldg(reinterpret_cast<const uint4*>(rv + (u + i) * 32));
                 }
             }
+            float acc[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const uint32_t lo[4] = {a[i].x, b[i].x, a[i].y, b[i].y}, hi[4] = {a[i].z, b[i].z, a[i].w, b[i].w};
-                mma_16816(acc, lo, x[i].x, x[i].y);
+                if (i == 0) mma_16816_0(acc, lo, x[i].x, x[i].y);
+                else mma_16816(acc, lo, x[i].x, x[i].y);
                 mma_16816(acc, hi, x[i].z, x[i].w);
             }
+            s0 += acc[0];
+            s1 += acc[2];
         }
         if (t == 0) {
-            red[un * kMixTile + g] = acc[0];
-            red[un * kMixTile + 8 + g] = acc[2];
+            red[un * kMixTile + g] = s0;
+            red[un * kMixTile + 8 + g] = s1;
         }
     }
     __syncthreads();

@@ -181,10 +181,10 @@ struct MixShrinkSmem {
 };
 constexpr int kMtShrinkThreads = 320;   // warps 0-7 sums, 8 copies, 9 products
 // The tensor core's running fp32 sum drops what falls below it, so an error grows with the number
-// of products added up in one: after kMtSeg stages (32 of them) the sum moves to registers, whose
+// of products added up in one: after kMtSeg stages (16 products) the sum moves to registers, whose
 // additions round (the weights' gradient of 8192 tokens of 3584 columns: 3.4e-6 off in norm with
-// sums of 1792 columns).
-constexpr int kMtSeg = 8;
+// sums of 1792 columns, 4e-7 with 256, in the same time).
+constexpr int kMtSeg = 4;
 
 // xmap: T rows of d columns, box 64 x 128; amap: Rp rows of d columns, box 64 x 32; 128-byte
 // swizzle both.  Grid: clusters of CS along x (shares of d), token tiles, y = chunks of NCH rows.

@@ -409,7 +409,7 @@ def _array(kind, items):
 def _rows(t, what: str) -> tuple[int, int, int]:
     """(rows, columns, row stride) of a 2-D bf16 tensor whose columns lie side by side."""
     shape = t.shape
-    if len(shape) != 2 or type_code(t.dtype) != LF_BF16:
+    if len(shape) != 2 or (_TYPE_CODES.get(t.dtype) if _TYPE_CODES else type_code(t.dtype)) != LF_BF16:
         raise ValueError(f"{what}: a 2-D bfloat16 tensor expected")
     n, c = shape
     ld, step = t.stride()
@@ -526,9 +526,10 @@ def lf_w4_quantize(W, group: int, q, scales, zeros=None, stream=None, check=True
 def lf_w4_dequantize(q, scales, zeros, group: int, W, stream=None, check=True) -> int:
     """W (d_out x d_in fp32, bf16 or fp16) = (q - zeros) * scales."""
     d_out, d_in = W.shape
+    code = type_code(W.dtype)
     _w4_tables(q, scales, zeros, d_out, d_in, int(group))
-    st = lib().lf_w4_dequantize(_ptr(q), _ptr(scales), _ptr(zeros), d_out, d_in, int(group), _ptr(W),
-                                type_code(W.dtype), _stream(stream))
+    st = lib().lf_w4_dequantize(_ptr(q), _ptr(scales), _ptr(zeros), d_out, d_in, int(group), _ptr(W), code,
+                                _stream(stream))
     return _check(st, "lf_w4_dequantize") if check else st
 
 
@@ -537,7 +538,7 @@ def _w4_tables(q, scales, zeros, d_out: int, d_in: int, group: int):
     n = d_out * (-(-d_in // group))
     if q.element_size() != 1 or q.numel() != d_out * (d_in // 2) or not q.is_contiguous():
         raise ValueError("q: a contiguous d_out x d_in / 2 uint8 tensor expected")
-    if scales.numel() != n or type_code(scales.dtype) != LF_BF16 or not scales.is_contiguous():
+    if scales.numel() != n or _TYPE_CODES.get(scales.dtype) != LF_BF16 or not scales.is_contiguous():
         raise ValueError("scales: a contiguous d_out x ceil(d_in / group) bfloat16 tensor expected")
     if zeros is not None and (zeros.numel() != n or zeros.element_size() != 1 or not zeros.is_contiguous()):
         raise ValueError("zeros: a contiguous d_out x ceil(d_in / group) uint8 tensor expected")
@@ -552,10 +553,11 @@ def make_w4_projection(x, y, q, scales, group: int, zeros=None, bias=None) -> lf
     if n != T or d_in != 2 * half or cols < d_out:
         raise ValueError(f"shapes do not fit: x {tuple(x.shape)}, y {tuple(y.shape)}, q {tuple(q.shape)}")
     _w4_tables(q, scales, zeros, d_out, d_in, group)
-    if bias is not None and (bias.numel() != d_out or type_code(bias.dtype) != LF_BF16 or not bias.is_contiguous()):
+    if bias is not None and (bias.numel() != d_out or _TYPE_CODES.get(bias.dtype) != LF_BF16 or not bias.is_contiguous()):
         raise ValueError("bias: d_out contiguous bfloat16 values expected")
-    p = lf_w4_projection(x.data_ptr(), y.data_ptr(), q.data_ptr(), scales.data_ptr(), _ptr(zeros), _ptr(bias), d_in,
-                         d_out, group, 0, x_ld, y_ld)
+    p = lf_w4_projection(x.data_ptr(), y.data_ptr(), q.data_ptr(), scales.data_ptr(),
+                         0 if zeros is None else zeros.data_ptr(), 0 if bias is None else bias.data_ptr(), d_in, d_out,
+                         group, 0, x_ld, y_ld)
     p.rows, p.device = T, x.device
     return p
 
