@@ -1109,16 +1109,21 @@ static bool encode_x_map(CUtensorMap* map, const void* x, int32_t T, int32_t d_i
 }
 
 // Whether a projection goes over the whole pool on the tensor cores: a pool of at most kMtRows
-// stacked rows (by the bound the caller gives), and a batch long enough.  Costs in us,
-// measured on 3584 x 3584 and 3584 x 18944: token by token, the factor rows of every slot from
-// L2 at about 5 TB/s (half the rank bound on average); dense, four launches and the packed
-// copy, then 6 operations per (token, stacked row, column) at about 600 TFLOP/s.
+// stacked rows (by the bound the caller gives), and a batch long enough.  Costs of one projection
+// in us, fitted to both paths measured on pools of 4 x 64, 16 x 16, 16 x 64 and 64 x 16 (adapters
+// x rank bound, ranks uniform below it), 2 and 6 slots, 3584 x 3584 and 4096 x 14336, 32 to 1024
+// tokens.  Token by token: 12, and the factor rows of every slot (half the bound on average) at
+// 10 TB/s.  Dense: 22 for the launches, 12 per 1024 rows, x and y at 3 TB/s, and 6 operations per
+// (token, row of the bound, column) at 6 POP/s (about half of the bound is there).  The choice is
+// within 15% of the better path at 165 of the 168 points, and within 36% at all.  At 16 x 16, 2 slots, 3584 x 3584 the
+// forward takes 20 against 25 us at 256 tokens, 26 against 25 at 512 and 39 against 26 at 1024.
 static bool mix_dense(int64_t T, int K, int64_t n_adapters, int max_rank, int64_t d_in, int64_t d_out) {
     const int64_t rmax = n_adapters * (max_rank > 0 ? max_rank : kMaxRank);
     if (rmax > kMtRows) return false;
     const double d = (double)(d_in + d_out), rank = 0.5 * (double)(max_rank > 0 ? max_rank : kMaxRank);
-    const double token = (double)T * K * rank * d * 2.0 / 5e6;
-    const double dense = 20.0 + (double)rmax * d * 4.0 / 3e6 + (double)T * (double)rmax * d * 6.0 / 6e8;
+    const double token = 12.0 + (double)T * K * rank * d * 2.0 / 10e6;
+    const double dense = 22.0 + (double)rmax * 12.0 / 1024.0 + (double)T * d * 2.0 / 3e6 +
+                         (double)T * (double)rmax * d * 6.0 / 6e9;
     return dense < token;
 }
 static int mix_rows(int64_t n_adapters, int max_rank) {   // rows of the packed matrices
