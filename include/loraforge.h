@@ -500,11 +500,15 @@ lf_status lf_route_experts_backward(int32_t T, const lf_router* router /*[host]*
  * row of the slice is (a token without valid slots gets its base row).
  * x: T rows of x_ld elements (multiple of 8).  Factor tables, pools, y_offset and max_rank
  * as for lf_lora_shrink_expand_slices.  1 <= top_k <= LF_ROUTER_MAX_K.  Projections of one
- * call must not write overlapping parts of any y, nor a y that another one reads.
+ * call must not write overlapping parts of any y, nor a y that another one reads, and no y
+ * may overlap an x.  ids, weights, adapter_scale and the tables need the alignment of their
+ * elements (LF_ERR_ALIGNMENT).
  * lf_lora_mixture_backward: gradients with the adapters held fixed (they are compressed
  * after training), per projection from dy (T rows of dy_ld, read at the slice's columns):
  *   dx_t = bf16( dx_base_t + sum_j w_tj s_j A'^T (B'^T dy_t) )   (dx NULL = not wanted;
- *          dx_base NULL = zeros, may be dx itself)
+ *          dx_base NULL = zeros, may be dx itself; no dx may overlap an x, a dy or what
+ *          another projection of the call reads or writes: projections that share x are
+ *          summed by calls one after the other, each with the last one's dx as its base)
  *   grad_weights[t][j] = sum over the call's projections of s_j <B'^T dy_t, A'_{e_tj} x_t>
  *          (fp32, in a fixed order; slots of -1 get 0; NULL = not wanted).
  * A long batch over a small pool (few stacked rows, n_adapters * max_rank; max_rank 0 counts
@@ -563,9 +567,10 @@ lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids,
  * lf_w4_dequantize: W0 to fp32 (exact), bf16 or fp16 (rounded once).
  * lf_w4_projections: for up to LF_MAX_PROJECTIONS projections of one token batch, in one
  * call, y_t = bf16( bias + sum_g scale_g sum_{c in g} (q_c - zero_g) x_tc ): products
- * exact, sums in fp32 (of (128 + q_c) x_tc and x_tc apart for up to 16 tokens), one rounding.  bias: nullable, d_out bf16.  x: T rows of x_ld, y: T
- * rows of y_ld, of which columns 0 .. d_out are written; x_ld and y_ld are multiples of 8;
- * projections may share x, but no y may overlap another y or an x.
+ * exact, sums in fp32 (of (128 + q_c) x_tc and x_tc apart for up to 16 tokens: there an
+ * infinite x gives NaN), one rounding.  bias: nullable, d_out bf16.  x: T rows of x_ld,
+ * y: T rows of y_ld, of which columns 0 .. d_out are written; x_ld and y_ld are multiples
+ * of 8; projections may share x, but no y may overlap another y or an x.
  * Errors: LF_ERR_INVALID_ARG (null pointers, negative counts, unknown type, x_ld < d_in,
  * y_ld < d_out, reserved not 0), LF_ERR_SHAPE (d_in not a positive multiple of 32, d_out < 1, another group),
  * LF_ERR_ALIGNMENT (q, x, y, W not 16-byte aligned, scales or bias not 2-byte aligned,

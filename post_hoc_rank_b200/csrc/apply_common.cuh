@@ -111,7 +111,7 @@ __device__ __forceinline__ bool factor_lookup(const int32_t* ranks, const int64_
     int err = 0;
     if (k > kMaxRank || (max_rank > 0 && k > max_rank)) err = LF_ERR_SHAPE;
     else if (k > 0 && ((oa & 7) || (ob & 7))) err = LF_ERR_ALIGNMENT;
-    else if (k > 0 && (oa < 0 || ob < 0 || oa + (int64_t)k * d_in > pool_A || ob + (int64_t)k * d_out > pool_Bt))
+    else if (k > 0 && (oa < 0 || ob < 0 || oa > pool_A - (int64_t)k * d_in || ob > pool_Bt - (int64_t)k * d_out))
         err = LF_ERR_WORKSPACE;
     if (err) {
         if (report) latch_error(err);

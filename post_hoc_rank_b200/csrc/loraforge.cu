@@ -557,7 +557,7 @@ static lf_status check_apply(int32_t d_in, const void* x, const void* y, int64_t
     if (!aligned16(x) || !aligned16(y)) return LF_ERR_ALIGNMENT;
     for (int q = 0; q < ns; ++q) {
         const lf_slice& t = sl[q];
-        if (t.d_out < 1 || t.pool_elems_A < 0 || t.pool_elems_Bt < 0 || t.y_offset < 0 || t.y_offset + t.d_out > y_ld ||
+        if (t.d_out < 1 || t.pool_elems_A < 0 || t.pool_elems_Bt < 0 || t.y_offset < 0 || t.y_offset > y_ld - t.d_out ||
             t.max_rank < 0 || t.max_rank > kMaxRank)
             return LF_ERR_INVALID_ARG;
         if (!shared && (!t.ranks || !t.off_A || !t.off_Bt)) return LF_ERR_INVALID_ARG;
@@ -1070,14 +1070,18 @@ static lf_status launch_mixture_token(const MixArgs& A, cudaStream_t s) {
     return LF_OK;
 }
 
-static lf_status check_mixture(int32_t T, int32_t K, const int32_t* ids, int32_t n_adapters, const void* projs,
-                               int32_t n_proj) {
+static lf_status check_mixture(int32_t T, int32_t K, const int32_t* ids, const float* weights, const float* scales,
+                               const float* grad_weights, int32_t n_adapters, const void* projs, int32_t n_proj) {
     if (T < 0 || n_adapters < 1 || n_adapters > 16384 || n_proj < 1 || n_proj > kMaxProj || !projs)
         return LF_ERR_INVALID_ARG;
     if (K < 1 || K > kMixMaxK) return LF_ERR_SHAPE;
     if ((int64_t)T * 8 > INT_MAX) return LF_ERR_SHAPE;   // grid
     if (T > 0 && !ids) return LF_ERR_INVALID_ARG;
+    if (!aligned4(ids) || !aligned4(weights) || !aligned4(scales) || !aligned4(grad_weights)) return LF_ERR_ALIGNMENT;
     return LF_OK;
+}
+static bool tables_aligned(const lf_slice& q) {
+    return aligned4(q.ranks) && !((reinterpret_cast<uintptr_t>(q.off_A) | reinterpret_cast<uintptr_t>(q.off_Bt)) & 7u);
 }
 
 static void mix_tables(MixProj& t, const lf_slice& q, int32_t d_in) {
@@ -1115,8 +1119,9 @@ static bool encode_x_map(CUtensorMap* map, const void* x, int32_t T, int32_t d_i
 // tokens.  Token by token: 12, and the factor rows of every slot (half the bound on average) at
 // 10 TB/s.  Dense: 22 for the launches, 12 per 1024 rows, x and y at 3 TB/s, and 6 operations per
 // (token, row of the bound, column) at 6 POP/s (about half of the bound is there).  The choice is
-// within 15% of the better path at 165 of the 168 points, and within 36% at all.  At 16 x 16, 2 slots, 3584 x 3584 the
-// forward takes 20 against 25 us at 256 tokens, 26 against 25 at 512 and 39 against 26 at 1024.
+// within 15% of the better path at 165 of the 168 points, and within 36% at all.  At 16 x 16,
+// 2 slots, 3584 x 3584 the forward takes 20 against 25 us at 256 tokens, 26 against 25 at 512 and
+// 39 against 26 at 1024.
 static bool mix_dense(int64_t T, int K, int64_t n_adapters, int max_rank, int64_t d_in, int64_t d_out) {
     const int64_t rmax = n_adapters * (max_rank > 0 ? max_rank : kMaxRank);
     if (rmax > kMtRows) return false;
@@ -1154,7 +1159,7 @@ static lf_status mix_projection(const lf_mixture_projection& q, MixProj& t) {
     const lf_status cs = check_apply(q.d_in, q.x, q.y, q.y_ld, &q.slice, 1, false);
     if (cs != LF_OK) return cs;
     if (q.x_ld < q.d_in) return LF_ERR_INVALID_ARG;
-    if ((q.x_ld & 7) || !aligned16(q.base)) return LF_ERR_ALIGNMENT;
+    if ((q.x_ld & 7) || !aligned16(q.base) || !tables_aligned(q.slice)) return LF_ERR_ALIGNMENT;
     mix_tables(t, q.slice, q.d_in);
     t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
     t.in2 = reinterpret_cast<const __nv_bfloat16*>(q.base);
@@ -1169,7 +1174,8 @@ static lf_status mix_projection(const lf_mixture_grad& q, MixProj& t) {
     const lf_status cs = check_apply(q.d_in, q.x, q.dy, q.dy_ld, &q.slice, 1, false);
     if (cs != LF_OK) return cs;
     if (q.x_ld < q.d_in || (q.dx && q.dx_ld < q.d_in) || (q.dx_base && !q.dx)) return LF_ERR_INVALID_ARG;
-    if ((q.x_ld & 7) || (q.dx && (q.dx_ld & 7)) || !aligned16(q.dx) || !aligned16(q.dx_base)) return LF_ERR_ALIGNMENT;
+    if ((q.x_ld & 7) || (q.dx && (q.dx_ld & 7)) || !aligned16(q.dx) || !aligned16(q.dx_base) || !tables_aligned(q.slice))
+        return LF_ERR_ALIGNMENT;
     mix_tables(t, q.slice, q.d_in);
     t.x = reinterpret_cast<const __nv_bfloat16*>(q.x);
     t.in2 = reinterpret_cast<const __nv_bfloat16*>(q.dy);
@@ -2452,7 +2458,7 @@ size_t lf_lora_mixture_backward_workspace_size(int32_t T, int32_t top_k, int32_t
 lf_status lf_lora_mixture(int32_t T, int32_t top_k, const int32_t* ids, const float* weights, int32_t n_adapters,
                           const lf_mixture_projection* projs, int32_t n_proj, float scale, const float* adapter_scale,
                           void* ws, size_t ws_bytes, lf_stream_t stream) {
-    const lf_status st = check_mixture(T, top_k, ids, n_adapters, projs, n_proj);
+    const lf_status st = check_mixture(T, top_k, ids, weights, adapter_scale, nullptr, n_adapters, projs, n_proj);
     if (st != LF_OK || T == 0) return st;
     MixArgs A{};
     A.T = T;
@@ -2477,7 +2483,7 @@ lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids,
                                    int32_t n_adapters, const lf_mixture_grad* projs, int32_t n_proj, float scale,
                                    const float* adapter_scale, float* grad_weights, void* ws, size_t ws_bytes,
                                    lf_stream_t stream) {
-    const lf_status st = check_mixture(T, top_k, ids, n_adapters, projs, n_proj);
+    const lf_status st = check_mixture(T, top_k, ids, weights, adapter_scale, grad_weights, n_adapters, projs, n_proj);
     if (st != LF_OK || T == 0) return st;
     MixArgs A{};
     A.T = T;

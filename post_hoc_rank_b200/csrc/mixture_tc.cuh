@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(256) mixture_pack_kernel(MixPackArgs a) {
             const int64_t oa = a.off_A[e], ob = a.off_Bt[e];
             if (k > kMaxRank || (a.max_rank > 0 && k > a.max_rank)) err = LF_ERR_SHAPE;
             else if (k > 0 && ((oa & 7) || (ob & 7))) err = LF_ERR_ALIGNMENT;
-            else if (k > 0 && (oa < 0 || ob < 0 || oa + (int64_t)k * a.d_in > a.pool_A || ob + (int64_t)k * a.d_out > a.pool_Bt))
+            else if (k > 0 && (oa < 0 || ob < 0 || oa > a.pool_A - (int64_t)k * a.d_in || ob > a.pool_Bt - (int64_t)k * a.d_out))
                 err = LF_ERR_WORKSPACE;
             if (err || k < 0) k = 0;
         }

@@ -242,6 +242,25 @@ def test_values_that_are_not_finite_stay_in_their_tokens(T, K, d_in, d_out):
     assert lf.lf_get_device_status() == 0
 
 
+@pytest.mark.parametrize("T", [4, 900])
+@pytest.mark.parametrize("side", ["offA", "offB"])
+def test_offsets_whose_end_passes_63_bits_are_refused(T, side):
+    b = Batch(T, 6, 3, 2048, 1096, 12, seed=9, empty=0.0, ranks=[4, 2, 3, 5, 6, 7])
+    b.ids[0] = [5, 2, 0]
+    keep = getattr(b, side)[2]
+    getattr(b, side)[2] = (1 << 63) - 8
+    D = b.dev()
+    y, dx = torch.empty_like(D["base"]), torch.empty_like(D["x"])
+    api.lora_mixture(D["ids"], D["w"], 6, [lf.make_mixture_projection(D["x"], y, b.slice(D), base=D["base"])], 1.0)
+    assert lf.lf_get_device_status() == 4
+    gw = api.lora_mixture_backward(D["ids"], D["w"], 6, [lf.make_mixture_grad(D["x"], D["dy"], dx, b.slice(D))], 1.0)
+    assert lf.lf_get_device_status() == 4 and not gw[D["ids"] == 2].any()
+    getattr(b, side)[2] = keep
+    ref = np.where(b.ids == 2, -1, b.ids)
+    want, mag = OR.mixture(b.x.float().numpy(), b.base.float().numpy(), ref, b.w, *b.pools(), 1.0)
+    check(y, want, mag, 2048 + 64 + 8)
+
+
 @pytest.mark.parametrize("K,d_in,d_out", [(2, 512, 512), (4, 2048, 2048)])
 def test_same_results_from_run_to_run_and_captured(K, d_in, d_out):
     b = Batch(512, 16, K, d_in, d_out, 64, seed=6)

@@ -98,6 +98,16 @@ def test_mixture_refusals(backward):
         assert mix(True, n_proj=2, wsb=16) == WORKSPACE
 
 
+@pytest.mark.parametrize("backward", [False, True])
+def test_mixture_refuses_misaligned_tables_and_far_slices(backward):
+    for bad in (dict(ids=18), dict(ranks=18), dict(off_A=20), dict(off_Bt=20)):
+        assert mix(backward, **bad) == ALIGNMENT, bad
+    if backward:
+        assert mix(True, gw=18) == ALIGNMENT
+    # y_offset + d_out past 63 bits
+    assert mix(backward, y_offset=(1 << 63) - 8) == INVALID
+
+
 def test_mixture_workspace_sizes():
     sl = a_slice(d_out=2048, max_rank=64)
     p = lf.lf_mixture_projection(16, None, 16, 2048, 0, 2048, 2048, sl)
