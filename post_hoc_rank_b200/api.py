@@ -271,11 +271,11 @@ def route_experts_backward(logits, router: lf.lf_router, ids, grad_weights, stre
     return grad
 
 
-def _same_rows(projections, T: int):
+def _same_rows(projections, T: int, device):
     for p in projections:
-        if p.rows == T:
+        if p.rows == T and p.device == device:
             continue
-        raise ValueError(f"every projection must have {T} rows, got {[p.rows for p in projections]}")
+        raise ValueError(f"every projection must have {T} rows on {device}, got {[(p.rows, p.device) for p in projections]}")
 
 
 def lora_mixture(ids, weights, n_adapters: int, projections, scale: float, adapter_scale=None, ws=None, stream=None):
@@ -286,7 +286,7 @@ def lora_mixture(ids, weights, n_adapters: int, projections, scale: float, adapt
     _expect(ids, "ids", dev, torch.int32, ids.shape)
     _expect(weights, "weights", dev, torch.float32, ids.shape)
     _expect(adapter_scale, "adapter_scale", dev, torch.float32, (n_adapters,))
-    _same_rows(projections, ids.shape[0])
+    _same_rows(projections, ids.shape[0], dev)
     with _on(dev, stream):
         projections = lf._array(lf.lf_mixture_projection, projections)
         if ws is None:
@@ -304,7 +304,7 @@ def lora_mixture_backward(ids, weights, n_adapters: int, grads, scale: float, ad
     _expect(ids, "ids", dev, torch.int32, ids.shape)
     _expect(weights, "weights", dev, torch.float32, ids.shape)
     _expect(adapter_scale, "adapter_scale", dev, torch.float32, (n_adapters,))
-    _same_rows(grads, ids.shape[0])
+    _same_rows(grads, ids.shape[0], dev)
     with _on(dev, stream):
         gw = torch.empty(ids.shape, dtype=torch.float32, device=dev) if grad_weights else None
         grads = lf._array(lf.lf_mixture_grad, grads)
@@ -357,9 +357,9 @@ def w4_dequantize(w4: W4, dtype=torch.bfloat16, stream=None):
 def w4_project(projections, stream=None):
     """y = x W0^T + bias for lf.make_w4_projection projections of one token batch
     (lf_w4_projections): all have the same number of rows of x."""
-    T = projections[0].rows
-    _same_rows(projections, T)
-    with _on(projections[0].device, stream):
+    T, dev = projections[0].rows, projections[0].device
+    _same_rows(projections, T, dev)
+    with _on(dev, stream):
         lf.lf_w4_projections(T, projections)
 
 

@@ -331,8 +331,22 @@ def lf_apply_slices_workspace_size(T: int, n_adapters: int, n_slices: int) -> in
 def make_slice(d_out, y_offset, ranks, off_A, off_Bt, A_pool, Bt_pool, max_rank=0) -> lf_slice:
     """lf_slice from device tensors (ranks int32, offsets int64, pools bf16); max_rank: 0, or
     an upper bound of the slice's ranks the caller knows."""
-    return lf_slice(int(d_out), int(max_rank), int(y_offset), _ptr(ranks), _ptr(off_A), _ptr(off_Bt), _ptr(A_pool),
-                    _ptr(Bt_pool), A_pool.numel(), Bt_pool.numel())
+    sl = lf_slice(int(d_out), int(max_rank), int(y_offset), _ptr(ranks), _ptr(off_A), _ptr(off_Bt), _ptr(A_pool),
+                  _ptr(Bt_pool), A_pool.numel(), Bt_pool.numel())
+    sl.devices = {t.device for t in (ranks, off_A, off_Bt, A_pool, Bt_pool) if hasattr(t, "device")}
+    return sl
+
+
+def _one_device(x, others, sl: lf_slice):
+    """x's device, which the other tensors (None: absent) and the slice's tables must share."""
+    dev = x.device
+    for t in others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"every tensor must live on x's device, {dev}, got {t.device}")
+    for d in getattr(sl, "devices", ()):
+        if d != dev:
+            raise ValueError(f"the slice's tables must live on x's device, {dev}, got {d}")
+    return dev
 
 
 def lf_lora_shrink_expand_slices(x, y, ids, n_adapters, slices, scale, ws, adapter_scale=None, seg_out=None,
@@ -453,13 +467,15 @@ def make_mixture_projection(x, y, sl: lf_slice, base=None) -> lf_mixture_project
     """lf_mixture_projection from device tensors: x T x d_in bf16, y T x y_ld bf16 (rows may be
     strided), base None (zeros) or laid out like y (y itself: in place)."""
     T, d_in, x_ld = _rows(x, "x")
-    n, _, y_ld = _rows(y, "y")
+    n, cols, y_ld = _rows(y, "y")
     if n != T:
         raise ValueError("x and y must have the same rows")
+    if sl.y_offset + sl.d_out > cols:
+        raise ValueError(f"the slice ends at column {sl.y_offset + sl.d_out}, y has {cols}")
     if base is not None and base is not y and (_rows(base, "base")[2] != y_ld or base.shape != y.shape):
         raise ValueError("base must have y's shape and row stride")
     p = lf_mixture_projection(x.data_ptr(), _ptr(base), y.data_ptr(), d_in, 0, x_ld, y_ld, sl)
-    p.rows = T
+    p.rows, p.device = T, _one_device(x, (y, base), sl)
     return p
 
 
@@ -467,9 +483,11 @@ def make_mixture_grad(x, dy, dx, sl: lf_slice, dx_base=None) -> lf_mixture_grad:
     """lf_mixture_grad from device tensors: x and dx T x d_in, dy T x dy_ld (bf16, rows may be
     strided); dx None = not wanted, dx_base None (zeros) or laid out like dx."""
     T, d_in, x_ld = _rows(x, "x")
-    n, _, dy_ld = _rows(dy, "dy")
+    n, cols, dy_ld = _rows(dy, "dy")
     if n != T:
         raise ValueError("x and dy must have the same rows")
+    if sl.y_offset + sl.d_out > cols:
+        raise ValueError(f"the slice ends at column {sl.y_offset + sl.d_out}, dy has {cols}")
     dx_ld = 0
     if dx is not None:
         if dx.shape != x.shape:
@@ -478,7 +496,7 @@ def make_mixture_grad(x, dy, dx, sl: lf_slice, dx_base=None) -> lf_mixture_grad:
     if dx_base is not None and (dx is None or _rows(dx_base, "dx_base")[2] != dx_ld or dx_base.shape != dx.shape):
         raise ValueError("dx_base must have dx's shape and row stride")
     p = lf_mixture_grad(x.data_ptr(), dy.data_ptr(), _ptr(dx_base), _ptr(dx), d_in, 0, x_ld, dy_ld, dx_ld, sl)
-    p.rows = T
+    p.rows, p.device = T, _one_device(x, (dy, dx, dx_base), sl)
     return p
 
 
@@ -559,6 +577,9 @@ def make_w4_projection(x, y, q, scales, group: int, zeros=None, bias=None) -> lf
                          0 if zeros is None else zeros.data_ptr(), 0 if bias is None else bias.data_ptr(), d_in, d_out,
                          group, 0, x_ld, y_ld)
     p.rows, p.device = T, x.device
+    for t in (y, q, scales, zeros, bias):
+        if t is not None and t.device != p.device:
+            raise ValueError(f"every tensor must live on x's device, {p.device}, got {t.device}")
     return p
 
 

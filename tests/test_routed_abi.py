@@ -197,6 +197,26 @@ def test_binding_refusals():
             bad()
 
 
+def test_binding_refuses_slices_past_the_columns_and_mixed_devices():
+    b = torch.bfloat16
+    x, wide = torch.zeros(4, 64, dtype=b), torch.zeros(4, 200, dtype=b)
+    y = wide[:, :96]                      # rows of 200, of which 96 columns are y's
+    pool = torch.zeros(1024, dtype=b)
+    at = lambda off: lf.make_slice(64, off, None, None, None, pool, pool)  # noqa: E731
+    lf.make_mixture_projection(x, y, at(32), base=y)
+    lf.make_mixture_grad(x, y, None, at(32))
+    m = torch.zeros(4, 64, dtype=b, device="meta")
+    there = lf.make_slice(64, 0, None, None, None, pool.to("meta"), pool)
+    q, s = torch.zeros(96, 32, dtype=torch.uint8), torch.zeros(96, 2, dtype=b)
+    for bad in (lambda: lf.make_mixture_projection(x, y, at(40)), lambda: lf.make_mixture_grad(x, y, None, at(40)),
+                lambda: lf.make_mixture_projection(x, m, at(0)), lambda: lf.make_mixture_projection(x, y, there),
+                lambda: lf.make_mixture_grad(x, m, None, at(0)), lambda: lf.make_mixture_grad(x, y, m, at(0)),
+                lambda: lf.make_mixture_grad(x, y, None, there), lambda: lf.make_w4_projection(x, y, q.to("meta"), s, 32),
+                lambda: lf.make_w4_projection(x, y, q, s, 32, bias=torch.zeros(96, dtype=b, device="meta"))):
+        with pytest.raises(ValueError):
+            bad()
+
+
 def test_flags_and_names_reach_the_structure():
     r = lf.make_router(64, 4, "sigmoid", n_groups=8, top_groups=3, group_top=2, renorm=False, weight_scale=2.5)
     assert (r.n_experts, r.top_k, r.score, r.n_groups, r.top_groups, r.group_top, r.renorm) == (64, 4, 1, 8, 3, 2, 0)
