@@ -333,19 +333,16 @@ def make_slice(d_out, y_offset, ranks, off_A, off_Bt, A_pool, Bt_pool, max_rank=
     an upper bound of the slice's ranks the caller knows."""
     sl = lf_slice(int(d_out), int(max_rank), int(y_offset), _ptr(ranks), _ptr(off_A), _ptr(off_Bt), _ptr(A_pool),
                   _ptr(Bt_pool), A_pool.numel(), Bt_pool.numel())
-    sl.devices = {t.device for t in (ranks, off_A, off_Bt, A_pool, Bt_pool) if hasattr(t, "device")}
+    sl.tables = (ranks, off_A, off_Bt, A_pool, Bt_pool)
     return sl
 
 
-def _one_device(x, others, sl: lf_slice):
-    """x's device, which the other tensors (None: absent) and the slice's tables must share."""
+def _one_device(x, others):
+    """x's device, which the other tensors (None: absent) must share."""
     dev = x.device
     for t in others:
-        if t is not None and t.device != dev:
+        if t is not None and getattr(t, "device", dev) != dev:   # raw addresses pass
             raise ValueError(f"every tensor must live on x's device, {dev}, got {t.device}")
-    for d in getattr(sl, "devices", ()):
-        if d != dev:
-            raise ValueError(f"the slice's tables must live on x's device, {dev}, got {d}")
     return dev
 
 
@@ -475,7 +472,7 @@ def make_mixture_projection(x, y, sl: lf_slice, base=None) -> lf_mixture_project
     if base is not None and base is not y and (_rows(base, "base")[2] != y_ld or base.shape != y.shape):
         raise ValueError("base must have y's shape and row stride")
     p = lf_mixture_projection(x.data_ptr(), _ptr(base), y.data_ptr(), d_in, 0, x_ld, y_ld, sl)
-    p.rows, p.device = T, _one_device(x, (y, base), sl)
+    p.rows, p.device = T, _one_device(x, (y, base, *getattr(sl, "tables", ())))
     return p
 
 
@@ -496,7 +493,7 @@ def make_mixture_grad(x, dy, dx, sl: lf_slice, dx_base=None) -> lf_mixture_grad:
     if dx_base is not None and (dx is None or _rows(dx_base, "dx_base")[2] != dx_ld or dx_base.shape != dx.shape):
         raise ValueError("dx_base must have dx's shape and row stride")
     p = lf_mixture_grad(x.data_ptr(), dy.data_ptr(), _ptr(dx_base), _ptr(dx), d_in, 0, x_ld, dy_ld, dx_ld, sl)
-    p.rows, p.device = T, _one_device(x, (dy, dx, dx_base), sl)
+    p.rows, p.device = T, _one_device(x, (dy, dx, dx_base, *getattr(sl, "tables", ())))
     return p
 
 
@@ -576,10 +573,7 @@ def make_w4_projection(x, y, q, scales, group: int, zeros=None, bias=None) -> lf
     p = lf_w4_projection(x.data_ptr(), y.data_ptr(), q.data_ptr(), scales.data_ptr(),
                          0 if zeros is None else zeros.data_ptr(), 0 if bias is None else bias.data_ptr(), d_in, d_out,
                          group, 0, x_ld, y_ld)
-    p.rows, p.device = T, x.device
-    for t in (y, q, scales, zeros, bias):
-        if t is not None and t.device != p.device:
-            raise ValueError(f"every tensor must live on x's device, {p.device}, got {t.device}")
+    p.rows, p.device = T, _one_device(x, (y, q, scales, zeros, bias))
     return p
 
 
