@@ -460,7 +460,8 @@ lf_status lf_lora_shrink_expand_noalloc(int32_t T, int32_t d_in, int32_t d_out,
  * lf_route_experts_backward: grad_logits (T rows of grad_ld, logits_type) from
  * grad_weights (T x top_k fp32) at the same logits and the forward's ids; the choice and
  * the bias have no gradient, slots of -1 are skipped, an id out of range latches
- * LF_ERR_BAD_INDEX and is skipped.  Every entry 0 .. E of every row is written.
+ * LF_ERR_BAD_INDEX and is skipped.  Every entry 0 .. E of every row is written, zeros where
+ * all slots are -1; grad_logits must not overlap logits.
  * Errors: LF_ERR_INVALID_ARG (null pointers, negative T, unknown score / type / flag,
  * a weight_scale that is not finite, row strides below E), LF_ERR_SHAPE (E outside
  * 1 .. LF_ROUTER_MAX_EXPERTS, top_k outside 1 .. min(E, LF_ROUTER_MAX_K), n_groups not a

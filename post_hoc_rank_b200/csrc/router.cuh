@@ -456,7 +456,8 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_experts_grad_kernel(R
     }
     const bool on = id >= 0;
     const float lj = on ? to_f32(row[id]) : -INFINITY;
-    const bool dense = !a.sigmoid && !a.renorm;
+    // a row without slots (a NaN in its logits among the reasons) gets zeros
+    const bool dense = !a.sigmoid && !a.renorm && __any_sync(0xffffffffu, on);
     float v;              // the slot's contribution to its entry
     float m = 0.f, inv = 0.f, G = 0.f;
     float l[EPL];
@@ -480,7 +481,7 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_experts_grad_kernel(R
         const float sj = on && m > -INFINITY ? expf(lj - m) * inv : 0.f;
         G = warp_sum(g * sj);
         v = g * sj;
-    } else if (a.renorm) {
+    } else if (a.renorm || !a.sigmoid) {   // (softmax here: no slots)
         const float ms = warp_max(lj);
         float r;
         if (!on || ms == -INFINITY) r = 0.f;

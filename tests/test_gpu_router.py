@@ -203,3 +203,21 @@ def test_captured_and_on_another_stream():
         want = R.choose(l.double().cpu().numpy(), 2, "softmax")
         assert (ids.cpu().numpy() == want).all()
         assert (cnt.cpu().numpy() == np.bincount(want.reshape(-1), minlength=E)).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("kw", [dict(renorm=False), dict(), dict(score="sigmoid", renorm=False), dict(score="sigmoid")])
+def test_rows_without_slots_have_no_gradient(dtype, kw):
+    l = np.random.default_rng(4).normal(size=(40, 70)).astype(np.float32)
+    l[3, 5], l[7, 69], l[9] = np.nan, np.inf, -np.inf
+    ld = torch.from_numpy(l).to(DT[dtype]).cuda()
+    r = lf.make_router(70, 4, **kw)
+    ids, w = api.route_experts(ld, r)
+    assert lf.lf_get_device_status() == 5
+    empty = (ids == -1).all(dim=1)
+    assert empty.nonzero().flatten().tolist() == [3, 7, 9] and not w[empty].any()
+    gw = torch.randn(40, 4, device="cuda")
+    gw[3] = float("nan")                  # slots that name no expert are not read
+    d = api.route_experts_backward(ld, r, ids, gw)
+    assert torch.isfinite(d).all() and not d[empty].any() and d[~empty].any(dim=1).all()
+    assert lf.lf_get_device_status() == 0
