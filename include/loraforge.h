@@ -450,8 +450,9 @@ lf_status lf_lora_shrink_expand_noalloc(int32_t T, int32_t d_in, int32_t d_out,
  *   ids[t][0 .. top_k): the experts with the largest c, in descending order;
  *   weights[t][j] = weight_scale * s (renorm 0) or weight_scale * s / sum of the chosen s
  *          (renorm 1; formed from ratios, so chosen scores that underflow keep theirs).
- * Ties, of experts and of groups, go to the lower index, and the choice is the one of
- * exact arithmetic: rows whose order fp32 cannot settle are decided in fp64.
+ * Ties, of experts and of groups, go to the lower index.  c_e is that of fp64: rows whose
+ * order fp32 cannot settle are decided there (sigmoids that both round to 1 there, of logits
+ * above 36.7, tie where their biases are equal; without a bias their logits decide).
  * Only a logit or bias of -inf shuts an expert out (a finite lowest value does not); where
  * fewer than top_k experts remain the last slots are id -1, weight 0, the form
  * lf_lora_mixture skips.  A NaN or +inf in a row's logits or in the bias latches

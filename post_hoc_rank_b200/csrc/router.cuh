@@ -13,8 +13,8 @@
 // 16.8 MB, 2.6 us); the instructions of the scores
 // and the rounds bound it.
 //
-// The chosen indices are exact: without a bias the key is the logit itself (both scores
-// are increasing), and a sum with a bias, formed in fp32, is trusted only where neighbours
+// The chosen indices are those of fp64 scores: without a bias the key is the logit itself (both
+// scores are increasing), and a sum with a bias, formed in fp32, is trusted only where neighbours
 // in the order are further apart than its rounding; a row with a closer pair is decided
 // again from fp64 scores, so the choice does not depend on how exp rounds.
 #pragma once
@@ -113,7 +113,8 @@ __device__ __noinline__ int route_row_f64(const RouterArgs& a, const TL* row, do
     for (int e = lane; e < a.E; e += 32) {
         const float l = to_f32(row[e]);
         const float b = a.bias ? a.bias[e] : 0.f;
-        const double s = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : c[e] / inv;
+        const double ex = exp(-fabs((double)l));   // no overflow on either side
+        const double s = a.sigmoid ? (l >= 0.f ? 1.0 : ex) / (1.0 + ex) : c[e] / inv;
         c[e] = l == -INFINITY || b == -INFINITY ? -INFINITY : s + (double)b;
     }
     __syncwarp();

@@ -221,3 +221,21 @@ def test_rows_without_slots_have_no_gradient(dtype, kw):
     d = api.route_experts_backward(ld, r, ids, gw)
     assert torch.isfinite(d).all() and not d[empty].any() and d[~empty].any(dim=1).all()
     assert lf.lf_get_device_status() == 0
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_scores_far_below_fp32_are_ordered(score):
+    """With a bias of zero the scores decide, and fp64 holds them down to logits of -740; equal
+    ones go to the lower index."""
+    l = np.full((4, 40), -np.inf, np.float32)
+    l[0, [1, 5, 33]] = [-100, -99, -101]
+    l[1, [1, 5, 33]] = [-650, -649, -651]
+    l[2, [1, 5, 33]] = [-700, -700, -690]
+    l[3, [1, 5, 33]] = [-720, -719, -717]
+    if score == "softmax":
+        l[:, 0] = 0
+    b = np.zeros(40, np.float32)
+    b[0] = -np.inf
+    ids, *_ = run(l, 3, bias=b, score=score)
+    assert (ids == R.choose(l, 3, score, b)).all()
+    assert ids[:, 0].tolist() == [5, 5, 33, 33]
