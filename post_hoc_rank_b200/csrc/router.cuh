@@ -15,8 +15,9 @@
 //
 // The chosen indices are those of fp64 scores: without a bias the key is the logit itself (both
 // scores are increasing), and a sum with a bias, formed in fp32, is trusted only where neighbours
-// in the order are further apart than its rounding; a row with a closer pair is decided
-// again from fp64 scores, so the choice does not depend on how exp rounds.
+// in the order are further apart than a bound of its rounding that holds for every expert of the
+// row (so that none that was not drawn can belong above); a row with a closer pair is decided
+// again from fp64 scores.
 #pragma once
 #include <cuda_fp16.h>
 
@@ -259,12 +260,22 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_experts_kernel(Router
         return;
     }
     if (a.bias) bmax = warp_max(bmax);
-    // Rounding of a score s, relative: the hardware exponential is within 2^-22 plus that of
-    // its argument (d = |l|, or m - l: 2 d 2^-24), the reciprocal and products add 2^-22, a
-    // softmax's sum EPL + 5 roundings; the sum with b is within 2^-24 of c, and the rounds below
-    // leave out its last log2(EPL) bits.  s <= |c| + |b|.  Two sums closer than both of their
-    // bounds may be out of order.
-    const float eps0 = 0x1p-20f + (float)EPL * 0x1p-22f + (a.sigmoid ? 0.f : (float)(EPL + 5) * 0x1p-23f);
+    // Error of a score, u = 2^-23, smax the row's largest score.  CUDA's bound for the hardware
+    // exponential is 2 + 1.173 |x| ulp, d = |x| (rounded before, for softmax: d / 2 ulp more), for
+    // __fdividef 2 ulp.
+    //   sigmoid: where l < 0, s (2 + 1.173 d + 1/2 + 2) u, and s d <= smax max(-m, 1), m the largest
+    //     logit; where l >= 0 (smax >= 1/2) only e / (1 + e) of the exponential's error: less.
+    //   softmax: s d <= 0.37 smax, so the numerator's is 2.62 u smax; the denominator's, weighted by
+    //     the scores, (2 + 1.673 ln E) u and (EPL + 5) / 2 u for its sum; its reciprocal and the
+    //     product 2.5 u.
+    // A sum s + b adds u / 2 of itself, the rounds below leave out EPL - 1 ulp of it.  So every
+    // expert's key is within err + rel |key| of its score and bias, the further down the lower
+    // still: two neighbours in the order that are further apart than both bounds order all that
+    // is above them and all that is below.  2^-120: scores that fp32 flushes or holds in few bits.
+    const float smax = a.sigmoid ? fast_sigmoid(m) : rden;
+    const float err = smax * (a.sigmoid ? 6.f + 1.25f * fminf(fmaxf(-m, 0.f), 104.f) : 22.f + 0.5f * (float)EPL) * 0x1p-23f +
+                      0x1p-120f;
+    const float rel = (float)(EPL + 1) * 0x1p-23f;
     bool close = false;
     if (a.G > 1) {
         float mine = kNoScore;   // score of group `lane`
@@ -313,8 +324,8 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_experts_kernel(Router
         if (scores) {   // the last group kept and the first left out
             const float lo = -warp_max(live && rank < a.top_groups ? -mine : -INFINITY);
             const float hi = warp_max(live && rank >= a.top_groups ? mine : -INFINITY);
-            // (d up to 104: what is further is below 2^-149)
-            close = hi > -INFINITY && lo - hi <= (eps0 + 208.f * 0x1p-24f) * (fabsf(lo) + fabsf(hi) + 4.f * bmax);
+            // one or two sums each, of at most smax + bmax, and their sum
+            close = hi > -INFINITY && lo - hi <= 4.f * err + 0x1p-22f * (smax + bmax) + 0x1p-23f * (fabsf(lo) + fabsf(hi));
         }
 #pragma unroll
         for (int i = 0; i < EPL; ++i) {
@@ -391,10 +402,20 @@ __global__ void __launch_bounds__(32 * kRouterWarps) route_experts_kernel(Router
         const float v = key_value(ckey), vn = __shfl_down_sync(0xffffffffu, v, 1);
         const float ln = __shfl_down_sync(0xffffffffu, el, 1), bn = __shfl_down_sync(0xffffffffu, eb, 1);
         const int cn = __shfl_down_sync(0xffffffffu, chosen, 1);
+        bool tie = false;   // equal inputs: a sure tie
         if (lane < a.K && chosen >= 0 && cn >= 0) {
-            const float d = fminf(a.sigmoid ? fmaxf(fabsf(el), fabsf(ln)) : m - fminf(el, ln), 104.f);
-            const float tol = (eps0 + d * 0x1p-23f) * (fabsf(v) + fabsf(vn) + fabsf(eb) + fabsf(bn));
-            close = close || (v - vn <= tol && !(el == ln && eb == bn));   // equal inputs: a sure tie
+            tie = el == ln && eb == bn;
+            close = close || (!tie && v - vn <= 2.f * err + rel * (fabsf(v) + fabsf(vn)));
+        }
+        if (__shfl_sync(0xffffffffu, (int)tie, a.K - 1)) {   // at the cut: what comes below the equal ones?
+            const float vk = __shfl_sync(0xffffffffu, v, a.K - 1), lk = __shfl_sync(0xffffffffu, el, a.K - 1);
+            const float bk = __shfl_sync(0xffffffffu, eb, a.K - 1);
+            for (int e = lane; e < E; e += 32) {
+                const float le = to_f32(row[e]), be = a.bias[e];
+                if (le == -INFINITY || be == -INFINITY || (le == lk && be == bk)) continue;
+                const float ce = (a.sigmoid ? fast_sigmoid(le) : __expf(le - m) * rden) + be;
+                close = close || fabsf(vk - ce) <= 2.f * err + rel * (fabsf(vk) + fabsf(ce));
+            }
         }
         close = __any_sync(0xffffffffu, close);
         if (lane == a.K) chosen = -1;   // the one left out

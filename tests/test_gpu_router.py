@@ -223,6 +223,80 @@ def test_rows_without_slots_have_no_gradient(dtype, kw):
     assert lf.lf_get_device_status() == 0
 
 
+def place(E, at, logits, biases, low, rest):
+    """A row of `low` logits (bias `rest`) with the given logits and biases at the experts `at`."""
+    l, b = np.full((1, E), low, np.float32), np.full(E, rest, np.float32)
+    l[0, at], b[at] = logits, biases
+    return l, b
+
+
+ONE = float(np.nextafter(np.float32(1), np.float32(2)))
+CUT = [
+    # an exact tie at the cut, and one expert a step above both that fp32 sums do not tell apart
+    (place(96, [0, 33, 66], [1, 1, ONE], 0.25, -5, 0), 1, 66),
+    (place(96, [0, 33, 66], [17, 17, 17.125], 0, -5, 0), 1, 66),
+    (place(96, [0, 33, 66], [0, 0, 0.0078125], 1e5, -5, 0), 1, 66),
+    (place(256, [3, 35, 67, 99], [1, 1, 1, ONE], 0.25, -5, 0), 2, 99),
+    # an expert whose bias takes nearly all of its score away, behind two that are small to begin with
+    (place(3, [0, 1, 2], [-17.8, -18.5, 1.1744667], [0, 0, -0.76395142], 0, 0), 1, 2),
+    (place(64, [0, 1, 2], [-13.629779, -13.630779, 4.8179813e-6], [0, 0, -0.5], -30, 0), 1, 2),
+]
+
+
+@pytest.mark.parametrize("i", range(len(CUT)))
+def test_the_last_choice_looks_past_the_first_one_left_out(i):
+    (l, b), K, first = CUT[i]
+    want = R.choose(l, K, "sigmoid", b)
+    assert want[0, 0] == first
+    ids, *_ = run(l, K, bias=b, score="sigmoid")
+    assert (ids == want).all()
+    for E in (128, 512, 1024):           # the same among more experts that are far below
+        if l.shape[1] < E:
+            wide, wb = np.full((1, E), -40, np.float32), np.full(E, -3, np.float32)
+            wide[:, :l.shape[1]], wb[:l.shape[1]] = l, b
+            ids, *_ = run(wide, K, bias=wb, score="sigmoid")
+            assert (ids == R.choose(wide, K, "sigmoid", wb)).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,tg", [(6, 1, 1), (64, 1, 1), (96, 3, 2), (250, 1, 1)])
+def test_biases_of_mixed_size_choose_exactly(score, E, G, tg):
+    """Biases that take away nearly all of a score, next to scores that are as small as what is
+    left; then far larger ones, which leave only some bits of the score."""
+    g = np.random.default_rng(E)
+    T = 500
+    l0 = (2 * g.normal(size=E)).astype(np.float32)
+    small = g.random(E) < 0.5
+    l0[small] -= 16
+    if score == "softmax":               # all scores but the first one's are small
+        l0[0] = 12
+    l = (l0 * (1 + g.integers(-4, 5, size=(T, E)) * 2.0 ** -22)).astype(np.float32)
+    near = np.where(small, 0, -R.scores(l0[None], score)[0]).astype(np.float32)
+    if score == "softmax":
+        near[0] = -np.inf
+    large = (near + g.choice([0.0, 1.0, 1e5, -1e9], size=E)).astype(np.float32)
+    for bias in (near, large):
+        for K in (1, 2, 5):
+            ids, *_ = run(l, K, bias=bias, score=score, n_groups=G, top_groups=tg, group_top=2 if G > 1 else 1)
+            assert (ids == R.choose(l, K, score, bias, G, tg, 2 if G > 1 else 1)).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,tg", [(40, 1, 1), (256, 8, 3), (900, 1, 1)])
+def test_ties_at_the_cut_with_biases(score, E, G, tg):
+    """Logits on a coarse grid and few biases: equal inputs at the cut in most rows, some of
+    them saturated, and sums that only nearly meet."""
+    g = np.random.default_rng(E + 1)
+    l = (np.round(g.normal(size=(300, E)) * 4) / 4).astype(np.float32)
+    l[:40] += 16                          # sigmoids next to 1
+    l[200:240] -= 30
+    for bias in (np.zeros(E), 0.25 * (np.arange(E) % 2), g.choice([0.0, 0.1, 0.1 + 2.0 ** -26], size=E)):
+        bias = bias.astype(np.float32)
+        for K in (1, 3, 8):
+            ids, *_ = run(l, K, bias=bias, score=score, n_groups=G, top_groups=tg, group_top=2 if G > 1 else 1)
+            assert (ids == R.choose(l, K, score, bias, G, tg, 2 if G > 1 else 1)).all()
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_scores_far_below_fp32_are_ordered(score):
     """With a bias of zero the scores decide, and fp64 holds them down to logits of -740; equal
