@@ -569,8 +569,7 @@ lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids,
  * lf_w4_dequantize: W0 to fp32 (exact), bf16 or fp16 (rounded once).
  * lf_w4_projections: for up to LF_MAX_PROJECTIONS projections of one token batch, in one
  * call, y_t = bf16( bias + sum_g scale_g sum_{c in g} (q_c - zero_g) x_tc ): products
- * exact, sums in fp32 (of (128 + q_c) x_tc and x_tc apart for up to 16 tokens: there an
- * infinite x gives NaN), one rounding.  bias: nullable, d_out bf16.  x: T rows of x_ld,
+ * exact, sums in fp32, one rounding.  bias: nullable, d_out bf16.  x: T rows of x_ld,
  * y: T rows of y_ld, of which columns 0 .. d_out are written; x_ld and y_ld are multiples
  * of 8; projections may share x, but no y may overlap another y or an x.
  * Errors: LF_ERR_INVALID_ARG (null pointers, negative counts, unknown type, x_ld < d_in,

@@ -287,11 +287,10 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(W4DequantArgs a) {
 // The reads bound it; what competes is the instructions of unpacking, about 60 per 512
 // bytes and warp, so the kernel spends none on anything else it can leave out:
 //  - a lane's 32-bit word gives nibbles i and i + 4 as a bf16 pair 128 + q by one mask (the
-//    columns of the product are permuted alike for x), and the 128 + z to subtract is taken
-//    out of the group's sum, sum (128 + q) x - (128 + z) sum x, instead of 4 subtractions per
-//    word; sum x comes from a product with ones, in the same accumulator layout.  Products
-//    and both sums are fp32; the difference loses at most the 5 bits that 128 + q is larger
-//    than q - z, far below the output's rounding (2^-19 of sum |w| |x|).
+//    columns of the product are permuted alike for x), and one packed subtraction makes q - z of
+//    it, exactly.  (Taking 128 + z out of the group's sum instead saves the subtractions, but
+//    leaves the rounding of 128 sum x where codes are near the zero point, and an x above 2^120
+//    overflows.)
 //  - with groups of 128 or more columns, lane t of a row takes the 16 bytes of unit t (32
 //    weights) of four, one 16-byte load for 4 words (WIDE); smaller groups, which end inside
 //    that, take word t of every unit.
@@ -319,12 +318,13 @@ struct alignas(64) W4Maps {
     CUtensorMap q[kW4MaxProj];     // d_out rows of d_in / 2 bytes, box 128 bytes x 32 rows, 128-byte swizzle
 };
 
-// bf16x2 of (128 + nibble i, 128 + nibble i + 4)
+// bf16x2 of (nibble i, nibble i + 4) - z, exact; z2: 128 + z twice
 template <int I>
-__device__ __forceinline__ uint32_t nibble_pair(uint32_t w) {
+__device__ __forceinline__ uint32_t nibble_pair(uint32_t w, uint32_t z2) {
     uint32_t r;
     asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w >> (4 * I)), "r"(0x000F000Fu), "r"(0x43004300u));
-    return r;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<__nv_bfloat162*>(&r), *reinterpret_cast<__nv_bfloat162*>(&z2));
+    return *reinterpret_cast<const uint32_t*>(&d);
 }
 template <int NT>
 struct W4Smem {
@@ -336,13 +336,14 @@ struct W4Smem {
 };
 
 // Sums of one warp over its columns: two 16-row tiles, NT token tiles; acc over all groups, part
-// and xs (sum x) over the current one.
+// over the current one.
 template <int NT>
 struct W4Acc {
-    float acc[2][NT][4], part[2][NT][4], xs[NT][4];
-    float sc[2][2], zn[2][2];   // scale and -(128 + z) of rows 16 m + 8 h + (this lane's row)
+    float acc[2][NT][4], part[2][NT][4];
+    float sc[2][2];             // scale of rows 16 m + 8 h + (this lane's row)
+    uint32_t z2[2][2];          // 128 + z of the same rows, twice (bf16)
 
-    // end of a group: acc += s (sum (128 + q) x - (128 + z) sum x)
+    // end of a group: acc += s sum (q - z) x
     __device__ __forceinline__ void flush() {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -350,16 +351,15 @@ struct W4Acc {
             for (int m = 0; m < 2; ++m)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const float2 d = ffma2(make_float2(zn[m][h], zn[m][h]), make_float2(xs[n][2 * h], xs[n][2 * h + 1]),
-                                           make_float2(part[m][n][2 * h], part[m][n][2 * h + 1]));
-                    const float2 r = ffma2(make_float2(sc[m][h], sc[m][h]), d,
+                    const float2 r = ffma2(make_float2(sc[m][h], sc[m][h]),
+                                           make_float2(part[m][n][2 * h], part[m][n][2 * h + 1]),
                                            make_float2(acc[m][n][2 * h], acc[m][n][2 * h + 1]));
                     acc[m][n][2 * h] = r.x;
                     acc[m][n][2 * h + 1] = r.y;
                 }
     }
     // scale and zero point of every row of the tile, one row per lane in sz: the scale's bf16 bits
-    // above those of -(128 + z)
+    // above those of 128 + z
     __device__ __forceinline__ void scales(uint32_t sz, int rg) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -367,13 +367,12 @@ struct W4Acc {
             for (int h = 0; h < 2; ++h) {
                 const uint32_t v = __shfl_sync(0xffffffffu, sz, 16 * m + 8 * h + rg);
                 sc[m][h] = __uint_as_float(v & 0xffff0000u);
-                zn[m][h] = __uint_as_float(v << 16);
+                z2[m][h] = __byte_perm(v, v, 0x1010);
             }
     }
     // one word of each of the lane's four rows against 8 columns of x; a group begins with FIRST
     template <bool FIRST>
     __device__ __forceinline__ void product(const uint32_t (&w)[2][2], const uint4 (&xv)[NT]) {
-        const uint32_t one[4] = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
         uint32_t b[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -381,16 +380,13 @@ struct W4Acc {
             b[n][1] = __byte_perm(xv[n].x, xv[n].z, 0x7632);   // (x1, x5)
             b[n][2] = __byte_perm(xv[n].y, xv[n].w, 0x5410);   // (x2, x6)
             b[n][3] = __byte_perm(xv[n].y, xv[n].w, 0x7632);   // (x3, x7)
-            if (FIRST) mma_16816_0(xs[n], one, b[n][0], b[n][1]);
-            else mma_16816(xs[n], one, b[n][0], b[n][1]);
-            mma_16816(xs[n], one, b[n][2], b[n][3]);
         }
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            const uint32_t lo[4] = {nibble_pair<0>(w[m][0]), nibble_pair<0>(w[m][1]), nibble_pair<1>(w[m][0]),
-                                    nibble_pair<1>(w[m][1])};
-            const uint32_t hi[4] = {nibble_pair<2>(w[m][0]), nibble_pair<2>(w[m][1]), nibble_pair<3>(w[m][0]),
-                                    nibble_pair<3>(w[m][1])};
+            const uint32_t lo[4] = {nibble_pair<0>(w[m][0], z2[m][0]), nibble_pair<0>(w[m][1], z2[m][1]),
+                                    nibble_pair<1>(w[m][0], z2[m][0]), nibble_pair<1>(w[m][1], z2[m][1])};
+            const uint32_t hi[4] = {nibble_pair<2>(w[m][0], z2[m][0]), nibble_pair<2>(w[m][1], z2[m][1]),
+                                    nibble_pair<3>(w[m][0], z2[m][0]), nibble_pair<3>(w[m][1], z2[m][1])};
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 if (FIRST) mma_16816_0(part[m][n], lo, b[n][0], b[n][1]);
@@ -494,7 +490,7 @@ __global__ void __launch_bounds__(32 * kW4Warps, 2) w4_gemv_kernel(const __grid_
             if (u >= units) break;   // uniform
             uint4 (&xc)[kUnits][NT] = xb[NT > 1 ? 0 : sb & 1];
             if (NT > 1) fetch_x(u, xc);
-            const uint32_t sz = ((uint32_t)__bfloat16_as_ushort(sn) << 16) | (zn & 15u) | 0xC300u;
+            const uint32_t sz = ((uint32_t)__bfloat16_as_ushort(sn) << 16) | (zn & 15u) | 0x4300u;
             int un = u + kUnits;     // the next step, in this block or the warp's next
             if (sb == kSteps - 1 || un >= units) un = u0 + 8 * kW4Warps;
             if (un < units) {

@@ -230,3 +230,53 @@ def test_a_layer_step_routed_over_4_bit_weights():
             tol = 2.0 ** -8 * (np.abs(want) + np.abs(y0) * (1 + 2.0 ** -8)) + \
                 (d_in * 2.0 ** -24 * 1.1) * m0 + (2.0 ** -18 + (d_in + 64) * 2.0 ** -24) * mag * 1.1
             assert (np.abs(y.double().cpu().numpy() - want) <= tol).all()
+
+
+def few(g, T, d_in, d_out, group, zp):
+    """(w4, codes less zero points, scales per column): codes equal the zero point but for some
+    columns, whose difference is -1 or 1."""
+    w4 = make(g, d_in, d_out, group, zp)
+    at = np.arange(d_in) // group
+    z = (w4.zeros.cpu().numpy().astype(np.int64) if zp else np.full((d_out, -(-d_in // group)), 8))[:, at]
+    step = np.where(z < 8, 1, -1) * (g.random((d_out, d_in)) < 0.03)
+    w4.q = torch.from_numpy(np.ascontiguousarray(OR.w4_pack((z + step).astype(np.uint8)))).cuda()
+    return w4, step.astype(np.float64), w4.scales.double().cpu().numpy()[:, at]
+
+
+@pytest.mark.parametrize("T", [1, 5, 8, 9, 16, 17, 40])
+@pytest.mark.parametrize("d_in,d_out,group,zp", [(96, 24, 32, True), (3584, 64, 128, True), (1056, 40, 256, False),
+                                                 (4096, 32, 64, True)])
+def test_columns_at_the_zero_point_add_nothing(T, d_in, d_out, group, zp):
+    """Large activations where the codes are the zero point leave no trace of 128 + q: the error
+    is within n 2^-24 (twice that, for sums that truncate) of the sum of |q - z| |s| |x| alone."""
+    g = np.random.default_rng(T + d_in)
+    w4, step, s = few(g, T, d_in, d_out, group, zp)
+    x = g.normal(size=(T, d_in))
+    x[:, (step == 0).all(axis=0) | (g.random(d_in) < 0.1)] *= 1000
+    x = torch.from_numpy(x.astype(np.float32)).bfloat16().cuda()
+    y = api.w4_linear(x, w4).double().cpu().numpy()
+    xn = x.double().cpu().numpy()
+    want, mag = xn @ (step * s).T, np.abs(xn) @ np.abs(step * s).T
+    assert (np.abs(y - want) <= 2.0 ** -8 * np.abs(want) + 1.01 * (d_in + 16) * 2.0 ** -23 * mag).all()
+    x = torch.where(torch.from_numpy((step == 0).all(axis=0)).cuda(), x, torch.zeros_like(x))
+    assert (api.w4_linear(x, w4) == 0).all()     # nothing but zero points
+
+
+@pytest.mark.parametrize("T", [1, 9, 16, 17])
+@pytest.mark.parametrize("group", [32, 128])
+def test_large_and_infinite_activations(T, group):
+    """A finite x of 2^123 (16 x, at most, is finite) gives finite products; an infinite one gives
+    an infinity of its weight's sign, NaN where that weight is 0."""
+    g = np.random.default_rng(group)
+    w4 = make(g, 256, 64, group, True)
+    M = OR.w4_matrix(w4.q.cpu().numpy(), w4.scales.double().cpu().numpy(), w4.zeros.cpu().numpy(), group)
+    x = torch.zeros(T, 256, dtype=torch.bfloat16, device="cuda")
+    x[:, 77] = 2.0 ** 123
+    y = api.w4_linear(x, w4).double().cpu().numpy()
+    want = np.broadcast_to(2.0 ** 123 * M[:, 77], y.shape)
+    assert (np.abs(y - want) <= 2.0 ** -8 * np.abs(want)).all()
+    x[T - 1, 77] = float("inf")
+    y = api.w4_linear(x, w4).double().cpu().numpy()
+    assert (np.abs(y - want)[:T - 1] <= 2.0 ** -8 * np.abs(want)[:T - 1]).all()
+    assert np.isnan(y[T - 1, M[:, 77] == 0]).all() and (M[:, 77] == 0).any()
+    assert (y[T - 1, M[:, 77] > 0] == np.inf).all() and (y[T - 1, M[:, 77] < 0] == -np.inf).all()
