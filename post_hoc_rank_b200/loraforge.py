@@ -330,7 +330,8 @@ def lf_apply_slices_workspace_size(T: int, n_adapters: int, n_slices: int) -> in
 
 def make_slice(d_out, y_offset, ranks, off_A, off_Bt, A_pool, Bt_pool, max_rank=0) -> lf_slice:
     """lf_slice from device tensors (ranks int32, offsets int64, pools bf16); max_rank: 0, or
-    an upper bound of the slice's ranks the caller knows."""
+    an upper bound of the slice's ranks the caller knows.  It holds the tensors, as what is made
+    of it does."""
     sl = lf_slice(int(d_out), int(max_rank), int(y_offset), _ptr(ranks), _ptr(off_A), _ptr(off_Bt), _ptr(A_pool),
                   _ptr(Bt_pool), A_pool.numel(), Bt_pool.numel())
     sl.tables = (ranks, off_A, off_Bt, A_pool, Bt_pool)
@@ -378,13 +379,15 @@ def lf_lora_shrink_expand_slices_routed(x, y, ids, n_adapters, slices, scale, ws
 def make_projection(x, y, sl: lf_slice) -> lf_projection:
     """lf_projection from device tensors: x T x d_in bf16, y T x y_ld bf16, and the slice
     (make_slice) saying where in y and with which factors."""
-    return lf_projection(_ptr(x), _ptr(y), int(x.shape[1]), 0, int(y.shape[1]), sl)
+    p = lf_projection(_ptr(x), _ptr(y), int(x.shape[1]), 0, int(y.shape[1]), sl)
+    p.holds = (x, y, sl)
+    return p
 
 
 def lf_lora_shrink_expand_projections(T, ids, n_adapters, projections, scale, ws=None, adapter_scale=None,
                                       stream=None, check=True) -> int:
     """Up to MAX_PROJECTIONS projections (make_projection) of one token batch in one call."""
-    arr = (lf_projection * len(projections))(*projections)
+    arr = _array(lf_projection, projections)
     st = lib().lf_lora_shrink_expand_projections(int(T), _ptr(ids), n_adapters, arr, len(projections), float(scale),
                                                  _ptr(adapter_scale), _ptr(ws), ws.numel() if ws is not None else 0,
                                                  _stream(stream))
@@ -407,14 +410,17 @@ _ARRAY_TYPES: dict = {}
 
 
 def _array(kind, items):
-    """C array of the structures in `items` (itself, if it is one already)."""
+    """C array of the structures in `items` (itself, if it is one already).  It holds them: a
+    structure in an array is a copy of the bytes, without the tensors that the item holds."""
     if isinstance(items, ctypes.Array):
         return items
     key = (kind, len(items))
     typ = _ARRAY_TYPES.get(key)
     if typ is None:
         typ = _ARRAY_TYPES[key] = kind * len(items)
-    return typ(*items)
+    arr = typ(*items)
+    arr.entries = tuple(items)
+    return arr
 
 
 def _rows(t, what: str) -> tuple[int, int, int]:
@@ -472,6 +478,7 @@ def make_mixture_projection(x, y, sl: lf_slice, base=None) -> lf_mixture_project
     if base is not None and base is not y and (_rows(base, "base")[2] != y_ld or base.shape != y.shape):
         raise ValueError("base must have y's shape and row stride")
     p = lf_mixture_projection(x.data_ptr(), _ptr(base), y.data_ptr(), d_in, 0, x_ld, y_ld, sl)
+    p.holds = (x, y, base, sl)
     p.rows, p.device = T, _one_device(x, (y, base, *getattr(sl, "tables", ())))
     return p
 
@@ -493,6 +500,7 @@ def make_mixture_grad(x, dy, dx, sl: lf_slice, dx_base=None) -> lf_mixture_grad:
     if dx_base is not None and (dx is None or _rows(dx_base, "dx_base")[2] != dx_ld or dx_base.shape != dx.shape):
         raise ValueError("dx_base must have dx's shape and row stride")
     p = lf_mixture_grad(x.data_ptr(), dy.data_ptr(), _ptr(dx_base), _ptr(dx), d_in, 0, x_ld, dy_ld, dx_ld, sl)
+    p.holds = (x, dy, dx, dx_base, sl)
     p.rows, p.device = T, _one_device(x, (dy, dx, dx_base, *getattr(sl, "tables", ())))
     return p
 
@@ -573,6 +581,7 @@ def make_w4_projection(x, y, q, scales, group: int, zeros=None, bias=None) -> lf
     p = lf_w4_projection(x.data_ptr(), y.data_ptr(), q.data_ptr(), scales.data_ptr(),
                          0 if zeros is None else zeros.data_ptr(), 0 if bias is None else bias.data_ptr(), d_in, d_out,
                          group, 0, x_ld, y_ld)
+    p.holds = (x, y, q, scales, zeros, bias)
     p.rows, p.device = T, _one_device(x, (y, q, scales, zeros, bias))
     return p
 

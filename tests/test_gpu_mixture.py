@@ -328,3 +328,33 @@ def test_empty_batch_and_module_of_zero_ranks():
         api.lora_mixture(D["ids"], D["w"], 3, [lf.make_mixture_projection(D["x"], y, b.slice(D))], 1.0)
         assert (y == 0).all()
     assert lf.lf_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_descriptions_of_temporaries(T):
+    """Inputs cast and tables made where the call describes them: their memory is not handed out
+    again (to the next one, to the workspace, to the gradient) before the call has read it."""
+    b = Batch(T, 8, 2, 2048, 1032, 32, seed=12)
+    D = b.dev()
+    n = 5
+    xs = [torch.randn(T, 2048, device="cuda") for _ in range(n)]
+    wide = {k: D[k].double() for k in ("ranks", "offA", "offB")}
+
+    def sl():
+        return lf.make_slice(1032, 0, wide["ranks"].int(), wide["offA"].long(), wide["offB"].long(), D["A"].clone(),
+                             D["Bt"].clone(), 32)
+    held = [(x.bfloat16(), torch.empty_like(D["base"])) for x in xs]
+    api.lora_mixture(D["ids"], D["w"], 8, [lf.make_mixture_projection(x, y, b.slice(D, max_rank=32), base=D["base"])
+                                           for x, y in held], 1.0)
+    ys = [torch.empty_like(D["base"]) for _ in range(n)]
+    api.lora_mixture(D["ids"], D["w"], 8, [lf.make_mixture_projection(x.bfloat16(), y, sl(), base=D["base"].clone())
+                                           for x, y in zip(xs, ys)], 1.0)
+    assert all(torch.equal(y, h[1]) for y, h in zip(ys, held))
+    dxs = [torch.empty_like(h[0]) for h in held]
+    gw = api.lora_mixture_backward(D["ids"], D["w"], 8, [lf.make_mixture_grad(h[0], D["dy"], dx, b.slice(D, max_rank=32))
+                                                         for h, dx in zip(held, dxs)], 1.0)
+    dx2 = [torch.empty_like(h[0]) for h in held]
+    g2 = api.lora_mixture_backward(D["ids"], D["w"], 8, [lf.make_mixture_grad(x.bfloat16(), D["dy"].clone(), dx, sl())
+                                                         for x, dx in zip(xs, dx2)], 1.0)
+    assert torch.equal(gw, g2) and all(torch.equal(a, c) for a, c in zip(dxs, dx2))
+    assert lf.lf_get_device_status() == 0

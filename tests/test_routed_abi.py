@@ -1,6 +1,7 @@
 """Refusals of the gate, routed side path and 4-bit entry points that need no GPU: argument
 errors are found on the host before any CUDA call, through the C ABI and in the binding."""
 import ctypes
+import weakref
 
 import numpy as np
 import pytest
@@ -221,3 +222,40 @@ def test_flags_and_names_reach_the_structure():
     r = lf.make_router(64, 4, "sigmoid", n_groups=8, top_groups=3, group_top=2, renorm=False, weight_scale=2.5)
     assert (r.n_experts, r.top_k, r.score, r.n_groups, r.top_groups, r.group_top, r.renorm) == (64, 4, 1, 8, 3, 2, 0)
     assert np.float32(r.weight_scale) == np.float32(2.5)
+
+
+def test_descriptions_hold_their_tensors():
+    """Tensors made in place (a cast input, a slice's tables) live as long as the description
+    that carries their addresses, and as the array that is made of descriptions."""
+    b = torch.bfloat16
+    new = lambda *shape, **kw: torch.zeros(*shape, dtype=kw.get("dtype", b))  # noqa: E731
+
+    def a_slice(seen):
+        t = [new(4, dtype=torch.int32), new(4, dtype=torch.int64), new(4, dtype=torch.int64), new(1024), new(1024)]
+        seen += [weakref.ref(v) for v in t]
+        return lf.make_slice(64, 0, *t)
+
+    def mixture(seen):
+        t = [new(4, 64), new(4, 96), new(4, 96)]
+        seen += [weakref.ref(v) for v in t]
+        return lf.make_mixture_projection(t[0], t[1], a_slice(seen), base=t[2])
+
+    def gradient(seen):
+        t = [new(4, 64), new(4, 96), new(4, 64), new(4, 64)]
+        seen += [weakref.ref(v) for v in t]
+        return lf.make_mixture_grad(t[0], t[1], t[2], a_slice(seen), dx_base=t[3])
+
+    def w4_one(seen):
+        t = [new(4, 64), new(4, 96), new(96, 32, dtype=torch.uint8), new(96, 2), new(96, 2, dtype=torch.uint8), new(96)]
+        seen += [weakref.ref(v) for v in t]
+        return lf.make_w4_projection(*t[:4], 32, zeros=t[4], bias=t[5])
+
+    for make, kind in ((mixture, lf.lf_mixture_projection), (gradient, lf.lf_mixture_grad), (w4_one, lf.lf_w4_projection)):
+        seen = []
+        p = make(seen)
+        assert all(r() is not None for r in seen), make
+        arr = lf._array(kind, [p])
+        del p
+        assert all(r() is not None for r in seen), make
+        del arr
+        assert all(r() is None for r in seen), make
