@@ -272,10 +272,9 @@ def route_experts_backward(logits, router: lf.lf_router, ids, grad_weights, stre
 
 
 def _same_rows(projections, T: int, device):
-    for p in projections:
-        if p.rows == T and p.device == device:
-            continue
-        raise ValueError(f"every projection must have {T} rows on {device}, got {[(p.rows, p.device) for p in projections]}")
+    have = lf._rows_device(projections)
+    if have != (T, device):
+        raise ValueError(f"every projection must have {T} rows on {device}, got {have[0]} on {have[1]}")
 
 
 def lora_mixture(ids, weights, n_adapters: int, projections, scale: float, adapter_scale=None, ws=None, stream=None):
@@ -357,8 +356,7 @@ def w4_dequantize(w4: W4, dtype=torch.bfloat16, stream=None):
 def w4_project(projections, stream=None):
     """y = x W0^T + bias for lf.make_w4_projection projections of one token batch
     (lf_w4_projections): all have the same number of rows of x."""
-    T, dev = projections[0].rows, projections[0].device
-    _same_rows(projections, T, dev)
+    T, dev = lf._rows_device(projections)
     with _on(dev, stream):
         lf.lf_w4_projections(T, projections)
 

@@ -423,6 +423,21 @@ def _array(kind, items):
     return arr
 
 
+def _rows_device(items):
+    """(rows, device) that the descriptions in `items` (make_*, or an array that _array made) share."""
+    items = getattr(items, "entries", items)
+    first = None
+    for p in items:
+        have = getattr(p, "rows", None), getattr(p, "device", None)
+        if have[0] is None or have != (first or have):
+            raise ValueError("projections of one call must come from make_* and share their rows and device, "
+                             f"got {have} beside {first}")
+        first = have
+    if first is None:
+        raise ValueError("one projection or more expected")
+    return first
+
+
 def _rows(t, what: str) -> tuple[int, int, int]:
     """(rows, columns, row stride) of a 2-D bf16 tensor whose columns lie side by side."""
     shape = t.shape

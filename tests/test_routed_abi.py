@@ -259,3 +259,30 @@ def test_descriptions_hold_their_tensors():
         assert all(r() is not None for r in seen), make
         del arr
         assert all(r() is None for r in seen), make
+
+
+def test_arrays_made_once_are_taken_and_bare_ones_refused():
+    """The entry points take what make_* returns, as a list, a tuple or an array made of it; an
+    array of bare structures says neither rows nor device and is refused, as is an empty one."""
+    b = torch.bfloat16
+    x, y = torch.zeros(4, 64, dtype=b), torch.zeros(4, 96, dtype=b)
+    pool = torch.zeros(1024, dtype=b)
+    sl = lf.make_slice(64, 0, None, None, None, pool, pool)
+    q, s = torch.zeros(96, 32, dtype=torch.uint8), torch.zeros(96, 2, dtype=b)
+    made = {lf.lf_mixture_projection: lf.make_mixture_projection(x, y, sl), lf.lf_mixture_grad: lf.make_mixture_grad(x, y, None, sl),
+            lf.lf_w4_projection: lf.make_w4_projection(x, y, q, s, 32)}
+    for kind, p in made.items():
+        for ok in ([p, p], (p, p), lf._array(kind, [p, p])):
+            assert lf._rows_device(ok) == (4, x.device)
+        other = type(p).from_buffer_copy(p)
+        for bad in ([], (kind * 2)(p, p), [p, other], lf._array(kind, [other])):
+            with pytest.raises(ValueError):
+                lf._rows_device(bad)
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    bare = {k: (k * 1)(p) for k, p in made.items()}
+    for bad in (lambda: api.lora_mixture(ids, None, 4, bare[lf.lf_mixture_projection], 1.0),
+                lambda: api.lora_mixture_backward(ids, None, 4, bare[lf.lf_mixture_grad], 1.0),
+                lambda: api.w4_project(bare[lf.lf_w4_projection]), lambda: api.w4_project([]),
+                lambda: api.lora_mixture(ids, None, 4, [], 1.0)):
+        with pytest.raises(ValueError):
+            bad()
