@@ -338,6 +338,39 @@ def make_slice(d_out, y_offset, ranks, off_A, off_Bt, A_pool, Bt_pool, max_rank=
     return sl
 
 
+_TABLE_TYPES: list = []
+
+
+def _adapters(sl: lf_slice):
+    """Number of adapters that the tables of a slice hold (None where they are raw addresses),
+    checked once per slice: a wrong type or length is read out of range on the device."""
+    n = getattr(sl, "adapters", False)
+    if n is not False:
+        return n
+    if not _TABLE_TYPES:
+        import torch
+        _TABLE_TYPES.extend((torch.int32, torch.int64, torch.int64, torch.bfloat16, torch.bfloat16))
+    n = None
+    for t, dtype in zip(getattr(sl, "tables", ()), _TABLE_TYPES):
+        if t is None or t.__class__ is int:
+            continue
+        if t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError("contiguous int32 ranks, int64 offsets and bfloat16 pools expected, "
+                             f"got {t.dtype} with strides {t.stride()}")
+        if dtype is not _TABLE_TYPES[3] and (n is None or t.numel() < n):
+            n = t.numel()
+    sl.adapters = n
+    return n
+
+
+def _cover(projections, n_adapters: int):
+    """Checks that every slice's tables hold n_adapters entries (read whatever the ids name)."""
+    for p in getattr(projections, "entries", projections):
+        n = getattr(p, "adapters", None)
+        if n is not None and n < n_adapters:
+            raise ValueError(f"the call names {n_adapters} adapters, the tables of a slice hold {n}")
+
+
 def _one_device(x, others):
     """x's device, which the other tensors (None: absent) must share."""
     dev = x.device
@@ -494,7 +527,7 @@ def make_mixture_projection(x, y, sl: lf_slice, base=None) -> lf_mixture_project
         raise ValueError("base must have y's shape and row stride")
     p = lf_mixture_projection(x.data_ptr(), _ptr(base), y.data_ptr(), d_in, 0, x_ld, y_ld, sl)
     p.holds = (x, y, base, sl)
-    p.rows, p.device = T, _one_device(x, (y, base, *getattr(sl, "tables", ())))
+    p.rows, p.device, p.adapters = T, _one_device(x, (y, base, *getattr(sl, "tables", ()))), _adapters(sl)
     return p
 
 
@@ -516,7 +549,7 @@ def make_mixture_grad(x, dy, dx, sl: lf_slice, dx_base=None) -> lf_mixture_grad:
         raise ValueError("dx_base must have dx's shape and row stride")
     p = lf_mixture_grad(x.data_ptr(), dy.data_ptr(), _ptr(dx_base), _ptr(dx), d_in, 0, x_ld, dy_ld, dx_ld, sl)
     p.holds = (x, dy, dx, dx_base, sl)
-    p.rows, p.device = T, _one_device(x, (dy, dx, dx_base, *getattr(sl, "tables", ())))
+    p.rows, p.device, p.adapters = T, _one_device(x, (dy, dx, dx_base, *getattr(sl, "tables", ()))), _adapters(sl)
     return p
 
 
@@ -535,6 +568,7 @@ def lf_lora_mixture(ids, weights, n_adapters, projections, scale, ws=None, adapt
     """Routed side path: ids T x top_k int32, weights T x top_k fp32 or None, up to MAX_PROJECTIONS
     projections (make_mixture_projection)."""
     T, K = ids.shape
+    _cover(projections, n_adapters)
     arr = _array(lf_mixture_projection, projections)
     st = lib().lf_lora_mixture(T, K, _ptr(ids), _ptr(weights), n_adapters, arr, len(projections), float(scale),
                                _ptr(adapter_scale), _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream))
@@ -545,6 +579,7 @@ def lf_lora_mixture_backward(ids, weights, n_adapters, grads, scale, grad_weight
                              stream=None, check=True) -> int:
     """Gradients of lf_lora_mixture for x (per projection, make_mixture_grad) and the weights."""
     T, K = ids.shape
+    _cover(grads, n_adapters)
     arr = _array(lf_mixture_grad, grads)
     st = lib().lf_lora_mixture_backward(T, K, _ptr(ids), _ptr(weights), n_adapters, arr, len(grads), float(scale),
                                         _ptr(adapter_scale), _ptr(grad_weights), _ptr(ws),

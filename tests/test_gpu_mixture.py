@@ -358,3 +358,19 @@ def test_descriptions_of_temporaries(T):
                                                          for x, dx in zip(xs, dx2)], 1.0)
     assert torch.equal(gw, g2) and all(torch.equal(a, c) for a, c in zip(dxs, dx2))
     assert lf.lf_get_device_status() == 0
+
+
+def test_arrays_made_once_and_refused_tables():
+    b = Batch(5, 4, 2, 64, 64, 8, seed=3)
+    D = b.dev()
+    y, y2 = torch.empty_like(D["base"]), torch.empty_like(D["base"])
+    sl = b.slice(D)
+    arr = lf._array(lf.lf_mixture_projection, [lf.make_mixture_projection(D["x"], y, sl, base=D["base"])])
+    api.lora_mixture(D["ids"], D["w"], 4, arr, 1.0)
+    api.lora_mixture(D["ids"], D["w"], 4, [lf.make_mixture_projection(D["x"], y2, sl, base=D["base"])], 1.0)
+    assert torch.equal(y, y2)
+    for call in (lambda: api.lora_mixture(D["ids"], D["w"], 5, arr, 1.0),
+                 lambda: api.lora_mixture_backward(D["ids"], D["w"], 5, [lf.make_mixture_grad(D["x"], D["dy"], None, sl)], 1.0)):
+        with pytest.raises(ValueError, match="adapters"):
+            call()
+    assert lf.lf_get_device_status() == 0

@@ -286,3 +286,30 @@ def test_arrays_made_once_are_taken_and_bare_ones_refused():
                 lambda: api.lora_mixture(ids, None, 4, [], 1.0)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_factor_tables_that_do_not_fit_are_refused():
+    """The device reads entries 0 .. n_adapters of ranks and offsets whatever the ids name, as
+    32- and 64-bit integers, and the pools as bf16 values side by side."""
+    b = torch.bfloat16
+    x, y = torch.zeros(4, 64, dtype=b), torch.zeros(4, 96, dtype=b)
+    pool, ids = torch.zeros(2048, dtype=b), torch.zeros(4, 2, dtype=torch.int32)
+    good = dict(ranks=torch.zeros(5, dtype=torch.int32), off_A=torch.zeros(6, dtype=torch.int64),
+                off_Bt=torch.zeros(6, dtype=torch.int64)[:5], A_pool=pool, Bt_pool=pool.view(32, 64))
+    both = (lambda sl: lf.make_mixture_projection(x, y, sl), lambda sl: lf.make_mixture_grad(x, y, None, sl))
+    for make in both:
+        make(lf.make_slice(64, 0, *good.values()))
+        for bad in (dict(ranks=good["ranks"].long()), dict(off_A=good["off_A"].int()), dict(off_Bt=good["off_Bt"].int()),
+                    dict(ranks=torch.zeros(10, dtype=torch.int32)[::2]), dict(off_A=torch.zeros(10, dtype=torch.int64)[::2]),
+                    dict(A_pool=pool.float()), dict(Bt_pool=pool.half()), dict(A_pool=pool[::2])):
+            with pytest.raises(ValueError):
+                make(lf.make_slice(64, 0, *dict(good, **bad).values()))
+    for short in (dict(), dict(ranks=good["ranks"][:3]), dict(off_A=good["off_A"][:3]), dict(off_Bt=good["off_Bt"][:3])):
+        sl = lf.make_slice(64, 0, *dict(good, **short).values())
+        n = 6 if not short else 4
+        p, g = lf.make_mixture_projection(x, y, sl), lf.make_mixture_grad(x, y, None, sl)
+        for call in (lambda: lf.lf_lora_mixture(ids, None, n, [p], 1.0, stream=0),
+                     lambda: lf.lf_lora_mixture_backward(ids, None, n, [g], 1.0, stream=0),
+                     lambda: lf.lf_lora_mixture(ids, None, n, lf._array(lf.lf_mixture_projection, [p]), 1.0, stream=0)):
+            with pytest.raises(ValueError, match="adapters"):
+                call()
