@@ -513,6 +513,7 @@ lf_status lf_route_experts_backward(int32_t T, const lf_router* router /*[host]*
  *          summed by calls one after the other, each with the last one's dx as its base)
  *   grad_weights[t][j] = sum over the call's projections of s_j <B'^T dy_t, A'_{e_tj} x_t>
  *          (fp32, in a fixed order; slots of -1 get 0; NULL = not wanted).
+ * A projection of which neither is wanted is checked and left out.
  * A long batch over a small pool (few stacked rows, n_adapters * max_rank; max_rank 0 counts
  * as 64) runs on the tensor cores as two dense products over the whole pool, with the
  * intermediates carried as two bf16 values (16 significant bits); other batches token by

@@ -1138,7 +1138,7 @@ static int mix_rows(int64_t n_adapters, int max_rank) {   // rows of the packed 
 struct MixTcWs {
     MixPlan* plan;
     __nv_bfloat16 *A, *Bt, *hi, *lo;
-    float *S, *U, *gw;
+    float *S, *U;
 };
 // Carves (base == nullptr: sizes) the dense path's workspace for one projection.
 static size_t carve_mix(void* base, int64_t T, int64_t Rp, int64_t d_in, int64_t d_out, bool grad, MixTcWs* w) {
@@ -2489,18 +2489,16 @@ lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids,
     A.T = T;
     A.K = top_k;
     A.n_adapters = n_adapters;
-    A.n_proj = n_proj;
     A.ids = ids;
     A.weights = weights;
     A.scale = scale;
     A.scales = adapter_scale;
-    bool any = grad_weights != nullptr;
-    for (int p = 0; p < n_proj; ++p) {
-        const lf_status ps = mix_projection(projs[p], A.p[p]);
+    for (int p = 0; p < n_proj; ++p) {   // those of which nothing is wanted are checked and left out
+        const lf_status ps = mix_projection(projs[p], A.p[A.n_proj]);
         if (ps != LF_OK) return ps;
-        any = any || projs[p].dx;
+        if (grad_weights || projs[p].dx) ++A.n_proj;
     }
-    if (!any) return LF_OK;
+    if (A.n_proj == 0) return LF_OK;
     const size_t need = mix_ws_size(T, top_k, n_adapters, projs, n_proj, true);
     if (need > 0 && !ws) return LF_ERR_INVALID_ARG;
     if (ws_bytes < need) return LF_ERR_WORKSPACE;

@@ -37,7 +37,6 @@ struct MixPlan {
     int32_t first[kMtRows + 1];    // per adapter (at most kMtRows of them with any rank): first stacked row
     int32_t rank[kMtRows];         // retained rank, 0 for one that fails the checks
     int32_t err[kMtRows];          // its error (latched by the tokens that use it)
-    int32_t expert[kMtRows];       // per stacked row: its adapter
     int32_t bad[2][kMtRows];       // per stacked row: its A, its B^T row holds a value that is not finite
 };
 
@@ -110,7 +109,6 @@ __global__ void __launch_bounds__(256) mixture_pack_kernel(MixPackArgs a) {
     const int d = is_a ? a.d_in : a.d_out;
     uint4* dst = reinterpret_cast<uint4*>((is_a ? a.A : a.Bt) + (int64_t)r * d);
     if (r >= R) {
-        if (is_a && tid == 0) a.plan->expert[r] = -1;
         if (tid == 0) a.plan->bad[blockIdx.y][r] = 0;
         for (int c = tid; c < d / 8; c += 256) dst[c] = make_uint4(0, 0, 0, 0);
         return;
@@ -122,7 +120,6 @@ __global__ void __launch_bounds__(256) mixture_pack_kernel(MixPackArgs a) {
         else hi = mid;
     }
     const int q = r - first[lo];
-    if (is_a && tid == 0) a.plan->expert[r] = lo;
     const uint4* src = reinterpret_cast<const uint4*>(is_a ? a.A_pool + a.off_A[lo] + (int64_t)q * d
                                                            : a.Bt_pool + a.off_Bt[lo] + (int64_t)q * d);
     // Products of the other tokens with this row are 0 times its values: what is not finite is

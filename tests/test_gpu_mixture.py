@@ -374,3 +374,22 @@ def test_arrays_made_once_and_refused_tables():
         with pytest.raises(ValueError, match="adapters"):
             call()
     assert lf.lf_get_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_projections_of_which_nothing_is_wanted_launch_nothing(T):
+    bs = [Batch(T, 8, 4, 2048, 2056, 64, seed=s) for s in (1, 2)]
+    Ds = [b.dev() for b in bs]
+    ids, w = Ds[0]["ids"], Ds[0]["w"]
+
+    def grads(dxs, ps):
+        n = lf.lf_launch_count()
+        api.lora_mixture_backward(ids, w, 8, [lf.make_mixture_grad(Ds[p]["x"], Ds[p]["dy"], dx, bs[p].slice(Ds[p]))
+                                              for p, dx in zip(ps, dxs)], 1.0, grad_weights=False)
+        return lf.lf_launch_count() - n
+    one, two = torch.empty_like(Ds[1]["x"]), torch.empty_like(Ds[1]["x"])
+    alone = grads([one], [1])
+    assert grads([None, two], [0, 1]) == alone and torch.equal(one, two)
+    assert grads([two, None], [1, 0]) == alone and torch.equal(one, two)
+    assert grads([None, None], [0, 1]) == 0
+    assert lf.lf_get_device_status() == 0
