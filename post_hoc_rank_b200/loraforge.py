@@ -480,7 +480,7 @@ def _rows(t, what: str) -> tuple[int, int, int]:
     ld, step = t.stride()
     if step != 1 and n > 0 and c > 1:
         raise ValueError(f"{what}: a unit column stride expected")
-    return n, c, (ld if n > 1 else max(ld, c))
+    return n, c, (ld if n > 1 else (c + 7) & ~7)   # a single row has no stride: any that is allowed
 
 
 def make_router(n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, top_groups: int = 1,

@@ -393,3 +393,16 @@ def test_projections_of_which_nothing_is_wanted_launch_nothing(T):
     assert grads([two, None], [1, 0]) == alone and torch.equal(one, two)
     assert grads([None, None], [0, 1]) == 0
     assert lf.lf_get_device_status() == 0
+
+
+def test_one_row_of_a_tensor_of_odd_width():
+    b = Batch(1, 4, 2, 64, 96, 8, seed=2, empty=0.0)
+    D = b.dev()
+    odd = torch.zeros(3, 201, dtype=torch.bfloat16, device="cuda")
+    odd[0, :64] = D["x"][0]
+    wide = torch.zeros(3, 208, dtype=torch.bfloat16, device="cuda")
+    y, want = wide[1:2, :96], torch.empty_like(D["base"])
+    api.lora_mixture(D["ids"], D["w"], 4, [lf.make_mixture_projection(odd[:1, :64], y, b.slice(D), base=D["base"])], 1.0)
+    api.lora_mixture(D["ids"], D["w"], 4, [lf.make_mixture_projection(D["x"], want, b.slice(D), base=D["base"])], 1.0)
+    assert torch.equal(y, want) and not wide[0].any() and not wide[2].any() and not wide[1, 96:].any()
+    assert lf.lf_get_device_status() == 0

@@ -313,3 +313,22 @@ def test_factor_tables_that_do_not_fit_are_refused():
                      lambda: lf.lf_lora_mixture(ids, None, n, lf._array(lf.lf_mixture_projection, [p]), 1.0, stream=0)):
             with pytest.raises(ValueError, match="adapters"):
                 call()
+
+
+def test_the_row_stride_of_a_single_row_does_not_matter():
+    b = torch.bfloat16
+    pool = torch.zeros(1024, dtype=b)
+    sl = lf.make_slice(64, 0, None, None, None, pool, pool)
+    odd, wide = torch.zeros(3, 201, dtype=b), torch.zeros(3, 200, dtype=b)
+    x, y = odd[:1, :64], wide[1:2, :96]
+    p = lf.make_mixture_projection(x, y, sl, base=torch.zeros(1, 96, dtype=b))
+    assert p.x_ld % 8 == 0 and p.x_ld >= 64 and p.y_ld % 8 == 0 and p.y_ld >= 96
+    g = lf.make_mixture_grad(x, y, wide[2:, :64], sl, dx_base=odd[:1, :64])
+    assert g.x_ld % 8 == g.dy_ld % 8 == g.dx_ld % 8 == 0
+    q, s = torch.zeros(96, 32, dtype=torch.uint8), torch.zeros(96, 2, dtype=b)
+    w = lf.make_w4_projection(x, odd[2:, :97], q, s, 32)
+    assert w.x_ld % 8 == w.y_ld % 8 == 0 and w.x_ld >= 64 and w.y_ld >= 96
+    for bad in (lambda: lf.make_mixture_projection(x, y, sl, base=torch.zeros(1, 88, dtype=b)),
+                lambda: lf.make_mixture_projection(odd[:2, :64], wide[:2, :96], sl, base=torch.zeros(2, 96, dtype=b))):
+        with pytest.raises(ValueError):
+            bad()
