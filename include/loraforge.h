@@ -563,10 +563,12 @@ lf_status lf_lora_mixture_backward(int32_t T, int32_t top_k, const int32_t* ids,
  *   or NULL = 8 everywhere;   W0[r][c] = (q[r][c] - zeros[r][g]) * scales[r][g].
  * lf_w4_quantize: from W (d_out x d_in, fp32 / bf16 / fp16).  zeros NULL: scale =
  * bf16(max|w| / 7), else scale = bf16((max(w, 0) - min(w, 0)) / 15) and zero =
- * clamp(rint(-min(w, 0) / scale), 0, 15); code = clamp(rint(w / scale) + zero, 0, 15);
- * quotients are exact before they are rounded, halves go to even; a group of zeros (or one
- * whose scale rounds to 0) has scale 0 and, with zeros, zero 0.  A value that is not
- * finite counts as 0 and latches LF_ERR_NUMERIC.
+ * clamp(rint(-min(w, 0) / scale), 0, 15); code = clamp(rint(w / scale) + zero, 0, 15).
+ * A scale's quotient is rounded to fp32 and that to bf16 (a quotient within 2^-24 of the
+ * middle of two bf16 values counts as the middle); the other quotients are exact before
+ * they are rounded; halves go to even.  A group of zeros (or one whose scale rounds to 0)
+ * has scale 0 and, with zeros, zero 0.  A value that is not finite counts as 0 and latches
+ * LF_ERR_NUMERIC.
  * lf_w4_dequantize: W0 to fp32 (exact), bf16 or fp16 (rounded once).
  * lf_w4_projections: for up to LF_MAX_PROJECTIONS projections of one token batch, in one
  * call, y_t = bf16( bias + sum_g scale_g sum_{c in g} (q_c - zero_g) x_tc ): products

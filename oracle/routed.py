@@ -149,7 +149,7 @@ def mixture_grad(x, dy, ids, w, ranks, off_A, off_Bt, A_pool, Bt_pool, scale, ad
 # ---- 4-bit base weights ---------------------------------------------------------------------
 
 def bf16(v):
-    """Nearest bf16 value (halves to even) of float64 values in its normal range."""
+    """bf16 value of float64 values in its normal range, by way of fp32 (halves to even, twice)."""
     u = np.asarray(v, dtype=np.float32).view(np.uint32).astype(np.uint64)
     u = (u + 0x7FFF + ((u >> 16) & 1)) & np.uint64(0xFFFF0000)
     return u.astype(np.uint32).view(np.float32).astype(np.float64)

@@ -22,7 +22,8 @@ namespace lf {
 // ---- quantisation ------------------------------------------------------------------------
 // Symmetric: s = bf16(max|w| / 7), z = 8.  With zero points: lo = min(w, 0), hi = max(w, 0),
 // s = bf16((hi - lo) / 15), z = clamp(rint(-lo / s), 0, 15).  q = clamp(rint(w / s) + z, 0, 15)
-// with the rounded s; every rint is of the exact quotient, halves to even.
+// with the rounded s; every rint is of the exact quotient, halves to even.  A scale is the bf16
+// value of the fp32 quotient: rounded twice, as fp32 code that fits scales rounds it.
 // G / 16 lanes per group, 16 weights each, the group's extremes by shuffles.  The read of W
 // bounds it (a bf16 18944 x 3584 matrix: 136 MB in, 36 MB out, 26 us) if the instructions
 // stay below it: scales by a product with a constant and quotients by a product with an
@@ -52,8 +53,9 @@ __device__ __forceinline__ float rint_quotient(float w, float s, float q) {
     return a > h || (a == h && odd) ? q + copysignf(1.f, e) : q;
 }
 
-// bf16((hi - lo) / den) of the exact quotient: a product with 1 / den unless that lands next
-// to the middle of two bf16 values (or near the ends of the range).
+// bf16(fp32((hi - lo) / den)): a product with 1 / den unless that lands next to the middle of two
+// bf16 values (or near the ends of the range), where the quotient is formed in fp64 and rounded
+// to fp32, then to bf16.
 __device__ __forceinline__ float bf16_quotient(float hi, float lo, float den) {
     float f = (hi - lo) * (1.f / den);
     const uint32_t low = __float_as_uint(f) & 0xffffu;

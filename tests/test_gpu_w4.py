@@ -280,3 +280,27 @@ def test_large_and_infinite_activations(T, group):
     assert (np.abs(y - want)[:T - 1] <= 2.0 ** -8 * np.abs(want)[:T - 1]).all()
     assert np.isnan(y[T - 1, M[:, 77] == 0]).all() and (M[:, 77] == 0).any()
     assert (y[T - 1, M[:, 77] > 0] == np.inf).all() and (y[T - 1, M[:, 77] < 0] == -np.inf).all()
+
+
+def test_scales_are_bf16_values_of_fp32_quotients():
+    """Quotients next to the middle of two bf16 values: fp32 makes the middle of them, which goes
+    to even; those that fp32 holds apart from it go to their side."""
+    W = torch.zeros(8, 32, device="cuda")
+    mid = 1 + 2.0 ** -8                                  # between 1 and 1 + 2^-7
+    W[0, 0], W[0, 1] = 15 * mid, -1e-9                   # above the middle by less than fp32 holds
+    W[1, 0] = 15 * mid
+    W[2, 0], W[2, 1] = 15 * mid, -2.0 ** -18             # by more
+    W[3, 0] = float(np.nextafter(np.float32(15 * mid), np.float32(0)))
+    W[4, 0], W[4, 1] = 15 * (1 + 3 * 2.0 ** -8), -1e-9   # between 1 + 2^-7 and 1 + 2^-6: up is even
+    W[5, 0] = float(np.nextafter(np.float32(15 * (1 + 3 * 2.0 ** -8)), np.float32(0)))
+    w4 = api.w4_quantize(W, 32, zero_points=True)
+    want = [1, 1, 1 + 2.0 ** -7, 1, 1 + 2.0 ** -6, 1 + 2.0 ** -7, 0, 0]
+    assert w4.scales[:, 0].tolist() == want
+    c, s, z = OR.w4_quantize(W.double().cpu().numpy(), 32, True)
+    assert s[:, 0].tolist() == want and (OR.w4_unpack(w4.q.cpu().numpy()) == c).all() and (w4.zeros.cpu().numpy() == z).all()
+    W /= 15
+    W *= 7
+    w4 = api.w4_quantize(W, 32)
+    c, s, z = OR.w4_quantize(W.double().cpu().numpy(), 32, False)
+    assert (w4.scales.double().cpu().numpy() == s).all() and (OR.w4_unpack(w4.q.cpu().numpy()) == c).all()
+    assert lf.lf_get_device_status() == 0
