@@ -229,7 +229,7 @@ def _on(device, stream=None):
         raise ValueError(f"tensors must live on a CUDA device, got {device}")
     if stream is not None:
         return torch.cuda.stream(torch.cuda.ExternalStream(stream, device) if isinstance(stream, int) else stream)
-    return _HERE if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+    return _HERE if device.index == lf.current_device() else torch.cuda.device(device)
 
 
 def _expect(t, name: str, device, dtype, shape):

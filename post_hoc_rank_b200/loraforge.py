@@ -240,11 +240,29 @@ def _mods_ptr(mods: np.ndarray):
     return mods.ctypes.data, int(mods.shape[0])
 
 
+_CUDA_NOW: list = []
+
+
+def _cuda_now():
+    """[current device, handle of a device's current stream].  torch.cuda.current_stream() builds a
+    Stream object to ask for its handle (3 us a call); torch's own calls under it give the handle
+    alone, and where a version of torch lacks them the public ones are taken."""
+    if not _CUDA_NOW:
+        import torch
+        device = getattr(torch._C, "_cuda_getDevice", None)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _CUDA_NOW.extend((device or torch.cuda.current_device,
+                          raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)))
+    return _CUDA_NOW
+
+
+def current_device() -> int:
+    return _cuda_now()[0]()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        # the handle alone: torch.cuda.current_stream() builds a Stream object, 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _cuda_now()[1](current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -332,3 +332,15 @@ def test_the_row_stride_of_a_single_row_does_not_matter():
                 lambda: lf.make_mixture_projection(odd[:2, :64], wide[:2, :96], sl, base=torch.zeros(2, 96, dtype=b))):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_the_current_stream_without_torchs_own_calls(monkeypatch):
+    class Stream:
+        def __init__(self, index):
+            self.cuda_stream = 1000 + index
+    monkeypatch.setattr(lf, "_CUDA_NOW", [])
+    for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda index=None: Stream(index))
+    assert lf.current_device() == 3 and lf._stream(None) == 1003 and lf._stream(7) == 7
