@@ -1228,7 +1228,9 @@ static lf_status launch_mix_shrink_n(const MixShrinkArgs& a, int Rmax, int cs, c
 static lf_status launch_mix_shrink(const MixShrinkArgs& a, int Rmax, const CUtensorMap& xmap, const CUtensorMap& amap,
                                    cudaStream_t s) {
     const int64_t tiles = cdiv(a.T, kMtM), steps = cdiv(a.d, kMtKB);
-    // chunks of 128 rows when even eight shares of d leave SMs idle with 256
+    // Chunks of 128 rows when even eight shares of d leave SMs idle with 256.  Both measured on pools
+    // of 4 x 64 to 16 x 64, 128 to 8192 tokens of 3584 columns: 128 against 256 in us, 256 rows of 333
+    // tokens 21 : 23, of 8192 43 : 39; 1024 rows of 333 tokens 21 : 23, of 700 29 : 23.
     const bool narrow = Rmax <= 128 || tiles * cdiv(Rmax, 256) * 8 < 148;
     const int64_t chunks = cdiv(Rmax, narrow ? 128 : 256);
     int cs = 1;   // shares of d: as many CTAs as SMs, eight stages or more each
@@ -2568,7 +2570,13 @@ lf_status lf_w4_projections(int32_t T, const lf_w4_projection* projs, int32_t n_
     int order[LF_MAX_PROJECTIONS];
     for (int p = 0; p < n_proj; ++p) order[p] = p;
     std::stable_sort(order, order + n_proj, [&](int u, int v) { return projs[u].d_in > projs[v].d_in; });
-    const bool many = T > 16;   // tcgen05 tiles of N tokens; few: the streaming kernel, 8 or 16 at a time
+    // Many tokens: tcgen05 tiles of N; few: the streaming kernel, 8 or 16 at a time.  Both measured at
+    // four shapes, groups of 64 and 128 and 1 .. 64 tokens, weights from HBM; streaming against
+    // tcgen05 in us, groups of 128, at 16 and at 17 tokens: 3584 x 18944 21 : 20 and 34 : 20, 18944 x
+    // 3584 25 : 26 and 33 : 26, 4096 x 4096 8 : 11 and 11 : 12; 3584 x 512 6.5 : 10 and 6.7 : 10 (fewer
+    // rows than SMs: streaming stays ahead up to 64 tokens).  N by the tokens (32, 64, 128 of them
+    // against the other tiles, 3584 x 18944: 20 : 21, 23; 21 : 37, 24; 25 : 70, 40).
+    const bool many = T > 16;
     const int N = T <= 32 ? 32 : T <= 64 ? 64 : 128;
     W4mMaps maps;
     std::memset(&maps, 0, sizeof(maps));

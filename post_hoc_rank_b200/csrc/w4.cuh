@@ -286,8 +286,10 @@ __global__ void __launch_bounds__(256) w4_dequantize_kernel(W4DequantArgs a) {
 // through a private ring of TMA stages (one box of 32 rows x 128 bytes each, 128-byte
 // swizzle, no block barriers), unpacks to bf16 and multiplies with mma.sync m16n8k16
 // (weights = the 16-row operand, tokens = the 8 columns): one product feeds up to 8 tokens.
-// The reads bound it; what competes is the instructions of unpacking, about 60 per 512
-// bytes and warp, so the kernel spends none on anything else it can leave out:
+// The reads bound it from below (a layer's 122 MB: 19 us); what competes is the instructions,
+// about 80 per 512 bytes and warp, and the waits that 16 warps per SM leave open (one token
+// through 7 projections: 37 us, issue slots 51 %, DRAM 39 % busy), so the kernel spends none on
+// anything it can leave out:
 //  - a lane's 32-bit word gives nibbles i and i + 4 as a bf16 pair 128 + q by one mask (the
 //    columns of the product are permuted alike for x), and one packed subtraction makes q - z of
 //    it, exactly.  (Taking 128 + z out of the group's sum instead saves the subtractions, but
