@@ -464,6 +464,8 @@ def _array(kind, items):
     """C array of the structures in `items` (itself, if it is one already).  It holds them: a
     structure in an array is a copy of the bytes, without the tensors that the item holds."""
     if isinstance(items, ctypes.Array):
+        if items._type_ is not kind:
+            raise TypeError(f"an array of {kind.__name__} expected, got {items._type_.__name__}")
         return items
     key = (kind, len(items))
     typ = _ARRAY_TYPES.get(key)

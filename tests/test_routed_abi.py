@@ -344,3 +344,17 @@ def test_the_current_stream_without_torchs_own_calls(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda index=None: Stream(index))
     assert lf.current_device() == 3 and lf._stream(None) == 1003 and lf._stream(7) == 7
+
+
+def test_arrays_of_other_structures_are_refused():
+    """An array's bytes are read as the entry point's own structure."""
+    made = {k: (k * 2)() for k in (lf.lf_projection, lf.lf_mixture_projection, lf.lf_mixture_grad, lf.lf_w4_projection)}
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    calls = {lf.lf_projection: lambda a: lf.lf_lora_shrink_expand_projections(4, ids, 4, a, 1.0, stream=0),
+             lf.lf_mixture_projection: lambda a: lf.lf_lora_mixture(ids, None, 4, a, 1.0, stream=0),
+             lf.lf_mixture_grad: lambda a: lf.lf_lora_mixture_backward(ids, None, 4, a, 1.0, stream=0),
+             lf.lf_w4_projection: lambda a: lf.lf_w4_projections(4, a, stream=0)}
+    for kind, call in calls.items():
+        for other, arr in made.items():
+            with pytest.raises(TypeError if other is not kind else lf.LFError):
+                call(arr)
